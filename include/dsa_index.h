@@ -70,6 +70,7 @@ extern "C" {
 #define DSA_ERR_TIMEOUT (-5)     /* a device-side bounded wait gave up */
 #define DSA_ERR_DEVICE (-6)      /* current device is not sm_100 */
 #define DSA_ERR_INTERNAL (-7)    /* a device-side consistency check failed */
+#define DSA_ERR_PAGES (-8)       /* a page plan needs more free pages than are left */
 
 /* group modes (PIVOT abstract: the Refine and Reuse variants; ADIndex —
  * Inference: refinement that also adds query-specific tokens) */

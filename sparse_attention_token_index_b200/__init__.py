@@ -1,7 +1,8 @@
-"""B200 (sm_100a) DSA lightning indexer: dense, group-shared (PIVOT) and decode.
+"""B200 (sm_100a) DSA lightning indexer: dense, group-shared (PIVOT) and decode,
+and the paged key-value cache whose tokens its answers select.
 
-A thin Python binding over the C ABI in ``include/dsa_index.h``
-(``libdsa_index.so``, built in-tree by ``sparse_attention_token_index_b200.build``).
+A thin Python binding over the C ABI in ``include/dsa_index.h`` and
+``include/dsa_paged.h`` (``libdsa_index.so``, built in-tree by ``sparse_attention_token_index_b200.build``).
 The functions here only marshal arguments: torch provides device memory and
 the current CUDA stream; every step of the indexer runs in the library's
 CUDA kernels.  There is no CPU path: without the library or a CUDA device
@@ -9,6 +10,7 @@ these functions raise.
 """
 from __future__ import annotations
 
+from . import _binding, _paged
 from ._binding import (  # noqa: F401
     DSA_DTYPE_BF16,
     DSA_DTYPE_FP32,
@@ -45,5 +47,15 @@ from ._binding import (  # noqa: F401
     decode_group_workspace_bytes,
     block_routed_workspace_bytes,
     ivf_routed_workspace_bytes,
-    EXPORTED_SYMBOLS,
 )
+from ._paged import (  # noqa: F401
+    dsa_page_plan,
+    dsa_page_append,
+    dsa_attend_paged,
+    dsa_attend_selected,
+    page_plan_workspace_bytes,
+    attend_paged_workspace_bytes,
+    attend_selected_workspace_bytes,
+)
+
+EXPORTED_SYMBOLS = _binding.EXPORTED_SYMBOLS + _paged.EXPORTED_SYMBOLS

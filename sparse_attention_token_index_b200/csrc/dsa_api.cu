@@ -273,6 +273,7 @@ const char* dsa_status_string(int status) {
     case DSA_ERR_TIMEOUT: return "device-side wait timed out";
     case DSA_ERR_DEVICE: return "device is not sm_100";
     case DSA_ERR_INTERNAL: return "device-side consistency check failed";
+    case DSA_ERR_PAGES: return "not enough free pages";
     default: return "unknown status";
   }
 }

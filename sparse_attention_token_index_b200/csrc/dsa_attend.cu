@@ -1,0 +1,361 @@
+// dsa_attend.cu — attention over the paged cache: the C entry points and the
+// general kernel.
+//
+// General kernel.  o = sum_s p_s v_s / sum_s p_s with p_s = exp(c q.k_s - m),
+// m the running maximum: one pass over the keys, the old sums scaled by
+// exp(m_old - m_new) whenever m grows.  A block of four warps takes one
+// (query row, head) and one part of the keys the row sees; each warp steps
+// through its share 32 keys at a time (a lane looks up one key's slot), and a
+// lane holds d / 32 elements of q and of the sums.  All fp32: it serves fp32
+// queries, where the weights' bf16 rounding of the tensor-core kernel would
+// not do, and head sizes that kernel has no tiles for.  Few rows are split
+// over the keys, and a second kernel joins the parts.
+#include <cmath>
+
+#include "dsa_paged.cuh"
+
+namespace dsa {
+
+constexpr int kGenWarps = 4;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(uint8_t x) { return e4m3_to_f32(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+template <typename TQ, typename TK, int kD>  // kD: elements of the head a lane holds
+__global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const AttendArgs a, int splits) {
+  const int64_t task = blockIdx.x;
+  const int split = (int)(task % splits);
+  const int64_t rh = task / splits;
+  const int row = (int)(rh / a.Hq), h = (int)(rh % a.Hq), hk = h / (a.Hq / a.Hkv);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RowSeq rs = find_row(a, row);
+  if (rs.b < 0) return;  // padding: its outputs stay
+  // entries this row scans: list entries, or the tokens up to its position
+  const int n = a.idx != nullptr ? a.k : max(0, rs.pos + 1);
+  const int chunk = (n + splits - 1) / splits;
+  const int n0 = min(n, split * chunk), n1 = min(n, n0 + chunk);
+  const TQ* q = static_cast<const TQ*>(a.Q) + ((int64_t)row * a.Hq + h) * a.d;
+  const TK* K = static_cast<const TK*>(a.K);
+  const TK* V = static_cast<const TK*>(a.V);
+  float qv[kD], o[kD], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kD; ++i) {
+    const int e = lane + 32 * i;
+    qv[i] = e < a.d ? to_f32(q[e]) * a.scale : 0.f;
+    o[i] = 0.f;
+  }
+  for (int s0 = n0 + warp * 32; s0 < n1; s0 += kGenWarps * 32) {
+    // this lane's key: element offset of its row, -1 when it is skipped
+    int64_t at = -1;
+    float ks = 1.f, vs = 1.f;
+    if (s0 + lane < n1) {
+      const int pos = a.idx != nullptr ? a.idx[(int64_t)row * a.k + s0 + lane] : s0 + lane;
+      if (pos >= 0 && pos <= rs.pos) {
+        int off;
+        const int id = page_of(a, rs.b, pos, off);
+        if (id >= 0) {
+          at = (int64_t)id * a.page_stride + ((int64_t)off * a.Hkv + hk) * a.d;
+          if (a.K_scale != nullptr) {
+            const int64_t sc = ((int64_t)id * a.page + off) * a.Hkv + hk;
+            ks = a.K_scale[sc];
+            vs = a.V_scale[sc];
+          }
+        }
+      }
+    }
+    const int cnt = min(32, n1 - s0);
+    for (int j0 = 0; j0 < cnt; j0 += 4) {
+      float s[4];
+      int64_t p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        p[j] = __shfl_sync(0xffffffffu, at, j0 + j);
+        float dot = 0.f;
+        if (p[j] >= 0) {
+#pragma unroll
+          for (int i = 0; i < kD; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.d) dot = fmaf(qv[i], to_f32(K[p[j] + e]), dot);
+          }
+        }
+        s[j] = dot;
+      }
+#pragma unroll
+      for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], w);
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[j] = p[j] >= 0 ? s[j] * __shfl_sync(0xffffffffu, ks, j0 + j) : -INFINITY;
+        top = fmaxf(top, s[j]);
+      }
+      if (top == -INFINITY) continue;  // nothing seen yet (the same on every lane)
+      const float keep = expf(m - top);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int i = 0; i < kD; ++i) o[i] *= keep;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (p[j] < 0) continue;
+        const float w = expf(s[j] - m);
+        l += w;
+        const float wv = w * __shfl_sync(0xffffffffu, vs, j0 + j);
+#pragma unroll
+        for (int i = 0; i < kD; ++i) {
+          const int e = lane + 32 * i;
+          if (e < a.d) o[i] = fmaf(wv, to_f32(V[p[j] + e]), o[i]);
+        }
+      }
+    }
+  }
+  // the warps' parts, joined in warp order
+  __shared__ float so[kGenWarps][kD * 32], sm[kGenWarps], sl[kGenWarps];
+#pragma unroll
+  for (int i = 0; i < kD; ++i) so[warp][lane + 32 * i] = o[i];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  float top = sm[0];
+#pragma unroll
+  for (int w = 1; w < kGenWarps; ++w) top = fmaxf(top, sm[w]);
+  float f[kGenWarps], sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kGenWarps; ++w) {
+    f[w] = sm[w] == -INFINITY ? 0.f : expf(sm[w] - top);
+    sum = fmaf(f[w], sl[w], sum);
+  }
+  const bool last = splits == 1;
+  const float inv = last ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+  for (int e = threadIdx.x; e < a.d; e += kGenWarps * 32) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kGenWarps; ++w) x = fmaf(f[w], so[w][e], x);
+    if (last)
+      put(static_cast<TQ*>(a.out) + rh * a.d + e, x * inv);
+    else
+      a.part_o[task * a.d + e] = x;
+  }
+  if (threadIdx.x == 0) {
+    if (last) {
+      if (a.lse != nullptr) a.lse[rh] = sum > 0.f ? top + logf(sum) : -INFINITY;
+    } else {
+      a.part_ml[2 * task] = top;
+      a.part_ml[2 * task + 1] = sum;
+    }
+  }
+}
+
+// Joins the `splits` parts of each (row, head): one warp each.
+template <typename TQ>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, int splits) {
+  const int64_t rh = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (rh >= (int64_t)a.total_q * a.Hq) return;
+  if (find_row(a, (int)(rh / a.Hq)).b < 0) return;
+  const float* ml = a.part_ml + 2 * rh * splits;
+  float top = -INFINITY, sum = 0.f;
+  for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[2 * s]);
+  for (int s = 0; s < splits; ++s)
+    if (ml[2 * s] != -INFINITY) sum = fmaf(expf(ml[2 * s] - top), ml[2 * s + 1], sum);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  for (int e = lane; e < a.d; e += 32) {
+    float x = 0.f;
+    for (int s = 0; s < splits; ++s)
+      if (ml[2 * s] != -INFINITY) x = fmaf(expf(ml[2 * s] - top), a.part_o[(rh * splits + s) * a.d + e], x);
+    put(static_cast<TQ*>(a.out) + rh * a.d + e, x * inv);
+  }
+  if (lane == 0 && a.lse != nullptr) a.lse[rh] = sum > 0.f ? top + logf(sum) : -INFINITY;
+}
+
+template <typename TQ, typename TK>
+static int run_general(const AttendArgs& a, int splits, cudaStream_t st) {
+  const unsigned grid = (unsigned)((int64_t)a.total_q * a.Hq * splits);
+  if (a.d <= 64)
+    attend_general_kernel<TQ, TK, 2><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+  else if (a.d <= 128)
+    attend_general_kernel<TQ, TK, 4><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+  else
+    attend_general_kernel<TQ, TK, 8><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+  if (splits > 1) {
+    const int64_t rh = (int64_t)a.total_q * a.Hq;
+    attend_join_kernel<TQ><<<(unsigned)((rh + 3) / 4), 128, 0, st>>>(a, splits);
+  }
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, cudaStream_t st) {
+  const NvtxRange nvtx(a.idx != nullptr ? "dsa.attend_selected" : "dsa.attend_paged");
+  if (q_dtype == DSA_DTYPE_FP32) return run_general<float, float>(a, splits, st);
+  if (kv_dtype == DSA_DTYPE_BF16) return run_general<__nv_bfloat16, __nv_bfloat16>(a, splits, st);
+  return run_general<__nv_bfloat16, uint8_t>(a, splits, st);
+}
+
+}  // namespace dsa
+
+using namespace dsa;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Parts of the keys a (row, head) is split into: enough blocks for eight a
+// multiprocessor, at most 64.
+int general_splits(int sms, int total_q, int Hq) {
+  const int64_t tasks = (int64_t)total_q * Hq, want = (int64_t)sms * 8;
+  const int64_t s = (want + tasks - 1) / tasks;
+  return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+}
+
+struct AttendPlan {
+  int splits;
+  size_t ml_off, o_off, total;
+};
+
+AttendPlan plan_general(int sms, int total_q, int Hq, int d) {
+  AttendPlan p;
+  p.splits = general_splits(sms, total_q, Hq);
+  const size_t parts = p.splits > 1 ? (size_t)total_q * Hq * p.splits : 0;
+  p.ml_off = sizeof(WsHeader);
+  p.o_off = p.ml_off + round256(parts * 8);
+  p.total = p.o_off + round256(parts * d * 4);
+  return p;
+}
+
+int check_attend(int B, int total_q, int Hq, int Hkv, int d, int q_dtype, int kv_dtype) {
+  if (B < 0 || total_q < 0 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv != 0) return DSA_ERR_INVALID_ARG;
+  if (Hq > 1024 || Hq / Hkv > 128 || d > 256 || B > (1 << 20)) return DSA_ERR_UNSUPPORTED;
+  if ((int64_t)total_q * Hq >= ((int64_t)1 << 30)) return DSA_ERR_UNSUPPORTED;
+  const bool f32 = q_dtype == DSA_DTYPE_FP32 && kv_dtype == DSA_DTYPE_FP32;
+  const bool b16 = q_dtype == DSA_DTYPE_BF16 && (kv_dtype == DSA_DTYPE_BF16 || kv_dtype == DSA_DTYPE_FP8_E4M3);
+  return f32 || b16 ? DSA_OK : DSA_ERR_UNSUPPORTED;
+}
+
+int attend_bytes(int B, int total_q, int Hq, int Hkv, int d, int q_dtype, int kv_dtype, size_t* bytes) {
+  if (!bytes) return DSA_ERR_INVALID_ARG;
+  int r = check_attend(B, total_q, Hq, Hkv, d, q_dtype, kv_dtype);
+  if (r != DSA_OK) return r;
+  *bytes = sizeof(WsHeader);
+  if (B == 0 || total_q == 0) return DSA_OK;
+  int sms = 0;
+  if ((r = current_device(nullptr, &sms)) != DSA_OK) return r;
+  *bytes = plan_general(sms, total_q, Hq, d).total;
+  return DSA_OK;
+}
+
+// Both forms; idx == nullptr: all cached tokens.
+int attend(AttendArgs& a, const float* softmax_scale, int q_dtype, int kv_dtype, void* workspace,
+           size_t workspace_bytes, void* stream) {
+  int r = check_attend(a.B, a.total_q, a.Hq, a.Hkv, a.d, q_dtype, kv_dtype);
+  if (r != DSA_OK) return r;
+  if (a.n_pages < 1 || a.page < 1 || a.max_pages < 1 || a.page_stride < (int64_t)a.page * a.Hkv * a.d)
+    return DSA_ERR_INVALID_ARG;
+  if ((int64_t)a.max_pages * a.page >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+  a.scale = softmax_scale != nullptr ? *softmax_scale : 1.f / std::sqrt((float)a.d);
+  if (!std::isfinite(a.scale)) return DSA_ERR_INVALID_ARG;
+  if (a.B == 0 || a.total_q == 0) return DSA_OK;
+  if (!a.Q || !a.K || !a.V || !a.table || !a.lens || !a.q_off || !a.out || !workspace) return DSA_ERR_INVALID_ARG;
+  const bool scaled = kv_dtype == DSA_DTYPE_FP8_E4M3;
+  if (scaled != (a.K_scale != nullptr) || scaled != (a.V_scale != nullptr)) return DSA_ERR_INVALID_ARG;
+  const uintptr_t elt = kv_dtype == DSA_DTYPE_FP32 ? 4 : (kv_dtype == DSA_DTYPE_BF16 ? 2 : 1);
+  if (!aligned16(a.Q) || !aligned16(a.out) || !aligned16(workspace) || reinterpret_cast<uintptr_t>(a.K) % elt ||
+      reinterpret_cast<uintptr_t>(a.V) % elt)
+    return DSA_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((r = current_device(nullptr, &sms)) != DSA_OK) return r;
+  const AttendPlan p = plan_general(sms, a.total_q, a.Hq, a.d);
+  if (workspace_bytes < p.total) return DSA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.status = reinterpret_cast<int*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + p.ml_off);
+  a.part_o = reinterpret_cast<float*>(ws + p.o_off);
+  return launch_attend_general(a, q_dtype, kv_dtype, p.splits, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int dsa_attend_paged_workspace_size(int B, int total_q, int max_q, int Hq, int Hkv, int d, int q_dtype,
+                                    int kv_dtype, size_t* bytes) {
+  if (max_q < 1 || max_q > 65536) return DSA_ERR_INVALID_ARG;
+  return attend_bytes(B, total_q, Hq, Hkv, d, q_dtype, kv_dtype, bytes);
+}
+
+int dsa_attend_paged(const void* Q, const void* K, const void* V, const float* K_scale, const float* V_scale,
+                     const int32_t* block_table, const int32_t* lens, const int32_t* q_offsets, int B, int total_q,
+                     int max_q, int n_pages, int page, int64_t page_stride, int max_pages, int Hq, int Hkv, int d,
+                     const float* softmax_scale, int q_dtype, int kv_dtype, void* out, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (max_q < 1 || max_q > 65536) return DSA_ERR_INVALID_ARG;
+  AttendArgs a{};
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.K_scale = K_scale;
+  a.V_scale = V_scale;
+  a.table = block_table;
+  a.lens = lens;
+  a.q_off = q_offsets;
+  a.B = B;
+  a.total_q = total_q;
+  a.max_q = max_q;
+  a.n_pages = n_pages;
+  a.page = page;
+  a.page_stride = page_stride;
+  a.max_pages = max_pages;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.out = out;
+  a.lse = lse;
+  return attend(a, softmax_scale, q_dtype, kv_dtype, workspace, workspace_bytes, stream);
+}
+
+int dsa_attend_selected_workspace_size(int B, int total_q, int k, int Hq, int Hkv, int d, int q_dtype, int kv_dtype,
+                                       size_t* bytes) {
+  if (k < 1 || k > 65536) return DSA_ERR_INVALID_ARG;
+  return attend_bytes(B, total_q, Hq, Hkv, d, q_dtype, kv_dtype, bytes);
+}
+
+int dsa_attend_selected(const void* Q, const void* K, const void* V, const float* K_scale, const float* V_scale,
+                        const int32_t* block_table, const int32_t* lens, const int32_t* q_offsets,
+                        const int32_t* idx, int k, int B, int total_q, int n_pages, int page, int64_t page_stride,
+                        int max_pages, int Hq, int Hkv, int d, const float* softmax_scale, int q_dtype, int kv_dtype,
+                        void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (k < 1 || k > 65536) return DSA_ERR_INVALID_ARG;
+  if (B > 0 && total_q > 0 && !idx) return DSA_ERR_INVALID_ARG;
+  AttendArgs a{};
+  a.Q = Q;
+  a.K = K;
+  a.V = V;
+  a.K_scale = K_scale;
+  a.V_scale = V_scale;
+  a.table = block_table;
+  a.lens = lens;
+  a.q_off = q_offsets;
+  a.idx = idx;
+  a.k = k;
+  a.B = B;
+  a.total_q = total_q;
+  a.n_pages = n_pages;
+  a.page = page;
+  a.page_stride = page_stride;
+  a.max_pages = max_pages;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.out = out;
+  a.lse = lse;
+  return attend(a, softmax_scale, q_dtype, kv_dtype, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// dsa_paged.cuh — what the paged-cache kernels share: the argument block, the
+// request a query row belongs to, the slot of a position, and the merge of
+// partial softmax results.
+#pragma once
+
+#include "dsa_common.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+
+// Arguments of both attention forms (idx == nullptr: all cached tokens).
+struct AttendArgs {
+  const void* Q;
+  const void* K;
+  const void* V;
+  const float* K_scale;
+  const float* V_scale;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* q_off;
+  const int32_t* idx;
+  int k;
+  int B, total_q, max_q;
+  int n_pages, page, max_pages;
+  int64_t page_stride;
+  int Hq, Hkv, d;
+  float scale;
+  void* out;
+  float* lse;
+  int* status;
+  // partial results of a split softmax (workspace)
+  float* part_o;
+  float* part_ml;
+};
+
+// The request of one query row: row `row` is query j = row - q0 of its m.
+struct RowSeq {
+  int b;     // request, -1: the row is padding or its request is not valid
+  int len;   // cached tokens, the new ones included
+  int pos;   // the row's position, -1 or below: it sees nothing
+};
+
+// Finds the request whose rows hold `row` (offsets ascend; a request without
+// rows is passed over).  Reports a request that breaks the call's rules.
+__device__ __forceinline__ RowSeq find_row(const AttendArgs& a, int row) {
+  RowSeq r;
+  r.b = -1;
+  r.len = 0;
+  r.pos = -1;
+  if (row >= a.q_off[a.B]) return r;  // padding behind the last request
+  int lo = 0, hi = a.B - 1;           // the last b with q_off[b] <= row
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.q_off[mid] <= row)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int q0 = a.q_off[lo], q1 = a.q_off[lo + 1], len = a.lens[lo];
+  if (q0 < 0 || row < q0 || row >= q1 || q1 > a.total_q || (a.idx == nullptr && q1 - q0 > a.max_q) || len < 0 ||
+      (int64_t)len > (int64_t)a.max_pages * a.page) {
+    report_error(a.status, DSA_ERR_INVALID_ARG, 40);
+    return r;
+  }
+  r.b = lo;
+  r.len = len;
+  r.pos = len - (q1 - q0) + (row - q0);
+  return r;
+}
+
+// Page id of `pos` of request b (0 <= pos < len), -1 if the table names a
+// page outside the pool; `off` is the offset within the page.
+__device__ __forceinline__ int page_of(const AttendArgs& a, int b, int pos, int& off) {
+  const int col = (int)((unsigned)pos / (unsigned)a.page);
+  off = pos - col * a.page;
+  const int id = a.table[(int64_t)b * a.max_pages + col];
+  if ((unsigned)id >= (unsigned)a.n_pages) {
+    report_error(a.status, DSA_ERR_INVALID_ARG, 41);
+    return -1;
+  }
+  return id;
+}
+
+// The general CUDA-core attention (dsa_attend.cu): `splits` parts a row.
+int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, cudaStream_t st);
+
+}  // namespace dsa
