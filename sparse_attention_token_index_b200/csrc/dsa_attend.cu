@@ -239,7 +239,24 @@ int check_attend(int B, int total_q, int Hq, int Hkv, int d, int q_dtype, int kv
   return f32 || b16 ? DSA_OK : DSA_ERR_UNSUPPORTED;
 }
 
-int attend_bytes(int B, int total_q, int Hq, int Hkv, int d, int q_dtype, int kv_dtype, size_t* bytes) {
+// Query rows that read the same cache, at most: the heads of a group, and
+// with all cached tokens a request's new queries (max_q; 1 for lists).
+int shared_rows(int max_q, int Hq, int Hkv) {
+  const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+  return rows < 128 ? (int)rows : 128;
+}
+
+// Either kernel may take the call (pages are not known yet): the larger need.
+size_t attend_need(int sms, int total_q, int max_q, int Hq, int Hkv, int d, int q_dtype) {
+  size_t n = plan_general(sms, total_q, Hq, d).total;
+  if (q_dtype == DSA_DTYPE_BF16 && d <= 128) {
+    const size_t tc = attend_tc_bytes(sms, shared_rows(max_q, Hq, Hkv), d);
+    n = tc > n ? tc : n;
+  }
+  return n;
+}
+
+int attend_bytes(int B, int total_q, int max_q, int Hq, int Hkv, int d, int q_dtype, int kv_dtype, size_t* bytes) {
   if (!bytes) return DSA_ERR_INVALID_ARG;
   int r = check_attend(B, total_q, Hq, Hkv, d, q_dtype, kv_dtype);
   if (r != DSA_OK) return r;
@@ -247,7 +264,7 @@ int attend_bytes(int B, int total_q, int Hq, int Hkv, int d, int q_dtype, int kv
   if (B == 0 || total_q == 0) return DSA_OK;
   int sms = 0;
   if ((r = current_device(nullptr, &sms)) != DSA_OK) return r;
-  *bytes = plan_general(sms, total_q, Hq, d).total;
+  *bytes = attend_need(sms, total_q, max_q, Hq, Hkv, d, q_dtype);
   return DSA_OK;
 }
 
@@ -271,10 +288,13 @@ int attend(AttendArgs& a, const float* softmax_scale, int q_dtype, int kv_dtype,
     return DSA_ERR_INVALID_ARG;
   int sms = 0;
   if ((r = current_device(nullptr, &sms)) != DSA_OK) return r;
-  const AttendPlan p = plan_general(sms, a.total_q, a.Hq, a.d);
-  if (workspace_bytes < p.total) return DSA_ERR_WORKSPACE;
+  const int max_q = a.idx != nullptr ? 1 : a.max_q;
+  if (workspace_bytes < attend_need(sms, a.total_q, max_q, a.Hq, a.Hkv, a.d, q_dtype)) return DSA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.status = reinterpret_cast<int*>(ws);
+  if (attend_tc_ok(a, q_dtype, kv_dtype))
+    return run_attend_tc(a, kv_dtype, shared_rows(max_q, a.Hq, a.Hkv), sms, ws, static_cast<cudaStream_t>(stream));
+  const AttendPlan p = plan_general(sms, a.total_q, a.Hq, a.d);
   a.part_ml = reinterpret_cast<float*>(ws + p.ml_off);
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
   return launch_attend_general(a, q_dtype, kv_dtype, p.splits, static_cast<cudaStream_t>(stream));
@@ -287,7 +307,7 @@ extern "C" {
 int dsa_attend_paged_workspace_size(int B, int total_q, int max_q, int Hq, int Hkv, int d, int q_dtype,
                                     int kv_dtype, size_t* bytes) {
   if (max_q < 1 || max_q > 65536) return DSA_ERR_INVALID_ARG;
-  return attend_bytes(B, total_q, Hq, Hkv, d, q_dtype, kv_dtype, bytes);
+  return attend_bytes(B, total_q, max_q, Hq, Hkv, d, q_dtype, kv_dtype, bytes);
 }
 
 int dsa_attend_paged(const void* Q, const void* K, const void* V, const float* K_scale, const float* V_scale,
@@ -323,7 +343,7 @@ int dsa_attend_paged(const void* Q, const void* K, const void* V, const float* K
 int dsa_attend_selected_workspace_size(int B, int total_q, int k, int Hq, int Hkv, int d, int q_dtype, int kv_dtype,
                                        size_t* bytes) {
   if (k < 1 || k > 65536) return DSA_ERR_INVALID_ARG;
-  return attend_bytes(B, total_q, Hq, Hkv, d, q_dtype, kv_dtype, bytes);
+  return attend_bytes(B, total_q, 1, Hq, Hkv, d, q_dtype, kv_dtype, bytes);
 }
 
 int dsa_attend_selected(const void* Q, const void* K, const void* V, const float* K_scale, const float* V_scale,

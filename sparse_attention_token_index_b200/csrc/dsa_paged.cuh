@@ -84,4 +84,10 @@ __device__ __forceinline__ int page_of(const AttendArgs& a, int b, int pos, int&
 // The general CUDA-core attention (dsa_attend.cu): `splits` parts a row.
 int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, cudaStream_t st);
 
+// The tensor-core attention (dsa_attend_tc.cu): whether it takes a call, and
+// its workspace, for at most `rows` query rows that read the same cache.
+bool attend_tc_ok(const AttendArgs& a, int q_dtype, int kv_dtype);
+size_t attend_tc_bytes(int sms, int rows, int d);
+int run_attend_tc(const AttendArgs& a, int kv_dtype, int rows, int sms, uint8_t* ws, cudaStream_t st);
+
 }  // namespace dsa
