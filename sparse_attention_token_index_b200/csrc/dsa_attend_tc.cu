@@ -258,11 +258,9 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[C]) {
   }
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -271,6 +269,62 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Four e4m3 bytes -> four bf16, exactly, in the order 0, 2, 1, 3: sign,
+// exponent and fraction move to their bf16 places, which reads as the value
+// times 2^-120 (the biases differ by 120), subnormals included.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
+  const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7b80), __ushort_as_bfloat16(0x7b80));  // 2^120
+  const uint32_t even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+  const uint32_t odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  const __nv_bfloat162 e = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&even), up);
+  const __nv_bfloat162 o = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&odd), up);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&e), *reinterpret_cast<const uint32_t*>(&o));
+}
+
+// True in one lane of a converged warp, always the same one; the compiler
+// knows that the branch is uniform, which tcgen05 operands profit from.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// A from tensor memory (lane: row, column: two bf16 along K), B from shared memory.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 __device__ __forceinline__ bool bar_or(int bar, int nthr, bool v) {
@@ -313,22 +367,29 @@ __device__ __forceinline__ float warp_columns(float (&v)[C]) {
 // ----------------------------------------------------------------------------
 // shared memory
 // ----------------------------------------------------------------------------
+constexpr int kTok = 8;  // tiles whose token masks and scales are kept: more than the ring can run ahead
+
 template <int N, int D, bool kFp8>
 struct Cfg {
+  static constexpr bool kRows = N == 128;            // query rows, not tokens, on the 128 lanes
   static constexpr int kChunks = D / 64;
   static constexpr int kSlotBytes = kTile * D * 2;   // one K or V tile, bf16
   static constexpr int kRawBytes = kTile * D;        // one e4m3 tile
   static constexpr int kQBytes = N * D * 2;
-  static constexpr int kQBufs = N <= (kFp8 ? 32 : 64) ? 2 : 1;
-  static constexpr int kPBytes = N * kTile * 2;
-  static constexpr int kPRow = N >= 64 ? 128 : N * 2;  // bytes of a P row (of its first 64 columns)
-  static constexpr int kRaw = kFp8 ? (N >= 128 && D >= 128 ? 3 : 4) : 0;
-  static constexpr int kOther = kQBufs * kQBytes + 2 * kPBytes + kRaw * kRawBytes;
-  static constexpr int kBudget = 232448 - 1024 - 8192;
+  static constexpr int kQBufs = kRows ? 1 : 2;
+  static constexpr int kPBytes = kRows ? 0 : N * kTile * 2;
+  static constexpr int kPRow = N >= 64 ? 128 : N * 2;  // bytes of a P row
+  static constexpr int kRaw = kFp8 ? (N == 64 && D == 128 ? 3 : 4) : 0;
+  static constexpr int kOther = kQBufs * kQBytes + 2 * kPBytes + kRaw * kRawBytes + (kFp8 ? kTok * kTile * 8 : 0);
+  static constexpr int kBudget = 232448 - 1024 - 6144;
   static constexpr int kFit = (kBudget - kOther) / kSlotBytes;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   static constexpr int kWarps = kSoftWarps + 1 + kLoadWarps;
-  static constexpr int kCols = N >= 128 ? 512 : (N >= 64 ? 256 : (N >= 32 ? 128 : 64));
+  // tensor memory: two score tiles, with rows on the lanes two tiles of bf16
+  // weights, and two output tiles (one where no more fit)
+  static constexpr int kSCols = N, kPCol = 2 * N, kOCol = kRows ? 2 * N + 128 : 2 * N, kOCols = kRows ? D : N;
+  static constexpr int kOBufs = kRows && D == 128 ? 1 : 2;
+  static constexpr int kCols = N == 128 ? 512 : 4 * N;
   static_assert(kSlots >= 2, "the ring holds a K and a V tile");
 };
 
@@ -337,15 +398,18 @@ struct AttendSmem {
   using C = Cfg<N, D, kFp8>;
   uint8_t ring[C::kSlots][C::kSlotBytes];
   uint8_t q[C::kQBufs][C::kQBytes];
-  uint8_t p[2][C::kPBytes];
+  uint8_t p[2][C::kPBytes ? C::kPBytes : 16];
   uint8_t raw[C::kRaw ? C::kRaw : 1][C::kRaw ? C::kRawBytes : 16];
+  float ksc[kTok][kFp8 ? kTile : 4], vsc[kTok][kFp8 ? kTile : 4];
+  uint32_t seen[kTok][4];
   uint64_t full[C::kSlots], empty[C::kSlots];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2];
-  uint64_t o_full, o_free, drain;
-  float red[2][4][N / 2];
-  float mref[N], fac[N], lsum[N];
-  int lim[N], orow[N];
+  uint64_t s_full[2], p_full[2], p_empty[2];
+  uint64_t o_full[2], o_free[2], tok_full[kTok], drain;
+  float red[2][4][N / 2 > 32 ? 32 : N / 2];
+  alignas(16) float nref[N];
+  float fac[N], lsum[2][N];
+  int lim[N], orow[2][N];
   int64_t sums[32];
   int64_t begin_off, total;
   int begin_b;
@@ -375,15 +439,15 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.q_full[i], kLoadWarps * 32);
+      mbar_init(&S.q_full[i], kFp8 ? kLoadWarps : kLoadWarps * 32);
       mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.s_empty[i], kSoftWarps);
       mbar_init(&S.p_full[i], kSoftWarps);
       mbar_init(&S.p_empty[i], 1);
+      mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.o_free[i], kSoftWarps);
     }
-    mbar_init(&S.o_full, 1);
-    mbar_init(&S.o_free, kSoftWarps);
+    for (int i = 0; i < kTok; ++i) mbar_init(&S.tok_full[i], kLoadWarps);
     mbar_init(&S.drain, 1);
     S.abort_flag = 0;
     S.begin_b = 0;
@@ -465,48 +529,97 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
     const int lw = warp - kMma - 1, tid = lw * 32 + lane;
     constexpr int kElt = kFp8 ? 1 : 2, kUnits = D * kElt / 16;  // 16-byte units of a cache row
     constexpr int kRowsAt = 32 / kUnits;                        // rows a warp copies at a time
+    constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
     const int unit = lane % kUnits, sub = lane / kUnits;
     const bool unit_ok = unit * 16 < a.d * kElt;
     const int64_t row_bytes = (int64_t)a.d * kElt;
     const uint8_t* pages[2] = {static_cast<const uint8_t*>(a.K) + unit * 16, static_cast<const uint8_t*>(a.V) + unit * 16};
+    const float c2 = a.scale * 1.44269504f;
     int fill = 0, qn = 0, ready = 0;  // tiles asked for, queries, e4m3 tiles converted
     bool ok = true;
+
+    // The lookup of a tile's tokens runs over two tiles, so that no load is
+    // waited for: list entries two tiles ahead, page ids one.
+    Walk<N, kSel> wa = walk;
+    Seg sa;
+    sa.tiles = 0;
+    int ja = 0;
+    int a_pos = -1, a_lim = 0, a_b = 0, a_hk = 0;   // entry of the tile after next
+    int b_id = -1, b_off = 0, b_hk = 0;             // page of the next tile's token
+    bool b_seen = false;
+    auto look_entry = [&]() {
+      a_pos = -1;
+      while (ja == sa.tiles) {
+        if (!wa.next(t, sa)) return;
+        ja = 0;
+        if (!sa.valid) sa.tiles = 0;
+      }
+      const int e = (sa.tile0 + ja) * kTile + tid;
+      ++ja;
+      if (e < sa.end) a_pos = kSel ? a.idx[(int64_t)sa.q0 * a.k + e] : e;
+      a_lim = kSel ? sa.lim0 : 0x7fffffff;
+      a_b = sa.b;
+      a_hk = sa.hk;
+    };
+    auto look_page = [&]() {
+      b_seen = a_pos >= 0 && a_pos <= a_lim;
+      b_hk = a_hk;
+      if (b_seen) {
+        const int col = (int)((unsigned)a_pos / (unsigned)a.page);
+        b_off = a_pos - col * a.page;
+        b_id = a.table[(int64_t)a_b * a.max_pages + col];
+      }
+    };
+    // mask and scales of a tile's tokens, for the softmax warps
+    int tok = 0;
+    uint32_t tok_seen = 0;
+    float tok_ks = 0.f, tok_vs = 0.f;
+    auto post_tokens = [&]() {
+      if constexpr (kFp8) {
+        S.ksc[tok % kTok][tid] = tok_ks * c2;
+        S.vsc[tok % kTok][tid] = tok_vs;
+      }
+      if (lane == 0) S.seen[tok % kTok][lw] = tok_seen;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tok_full[tok % kTok]);
+      ++tok;
+    };
     auto convert = [&]() {  // e4m3 tile `ready`: this thread's bytes, staged -> ring
       const int r = ready % C::kSlots;
       ok = ok && mbar_wait<true>(&S.empty[r], ((ready / C::kSlots) & 1) ^ 1, abort_flag, a.status, 76, budget);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
-      const uint8_t* src = S.raw[ready % C::kRaw] + tid * 16;
+      const uint8_t* src = S.raw[ready % kRaw] + tid * 16;
+      // the second 64-element chunk's lanes write their odd unit first, so that no two lanes of a row share banks
+      const int flip = (unit >> 2) & 1;
       uint8_t* dst0 = S.ring[r] + (unit >> 2) * kTile * 128;
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const uint4 raw = *reinterpret_cast<const uint4*>(src + i * kLoadWarps * 512);
-        uint32_t w[8];
-        const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __half2_raw h =
-              __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-          w[e] = *reinterpret_cast<const uint32_t*>(&b);
-        }
+        const uint2 w0 = e4m3x4_to_bf16(raw.x), w1 = e4m3x4_to_bf16(raw.y), w2 = e4m3x4_to_bf16(raw.z),
+                    w3 = e4m3x4_to_bf16(raw.w);
+        const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
         const int row = lw * 32 + i * kRowsAt + sub, u0 = (unit & 3) * 2, sw = row & 7;
         uint8_t* dst = dst0 + row * 128;
-        *reinterpret_cast<uint4*>(dst + ((u0 ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(dst + (((u0 + 1) ^ sw) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(dst + (((u0 + flip) ^ sw) << 4)) = flip ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + (((u0 + (flip ^ 1)) ^ sw) << 4)) = flip ? lo : hi;
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.full[r]);
       ++ready;
     };
+
+    look_entry();
+    look_page();
+    look_entry();
     while (ok && walk.next(t, s)) {
       if (!s.valid) continue;
       {  // the segment's queries
         const int qb = qn % C::kQBufs;
         if (kFp8 && C::kQBufs == 1) {
           // the only query buffer is free once the last keys, still staged, are multiplied
+          if (tok * 2 < fill) post_tokens();
           asm volatile("cp.async.wait_all;" ::: "memory");
           while (ok && ready < fill) convert();
         }
@@ -516,39 +629,59 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
         if (!ok) break;
         const uint8_t* Q = static_cast<const uint8_t*>(a.Q);
         constexpr int kQUnits = D / 8;
+#pragma unroll 4
         for (int e = tid; e < N * kQUnits; e += kLoadWarps * 32) {
           const int r = e / kQUnits, u = e % kQUnits, rr = s.row0 + r, j = rr / g;
           const bool in = r < s.rows && u * 8 < a.d;
           const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
-          copy16(smem_u32(S.q[qb]) + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4), Q + at * 2, in);
-        }
-        copies_arrive(&S.q_full[qb]);
-        ++qn;
-      }
-      auto cache_row = [&](int tile) {  // cache row of this thread's token, -1: none
-        const int e = tile * kTile + tid;
-        int pos = -1;
-        if (e < s.end) {
-          pos = e;
-          if constexpr (kSel) {
-            pos = a.idx[(int64_t)s.q0 * a.k + e];
-            if (pos > s.lim0) pos = -1;
+          uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+          if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in) v = *reinterpret_cast<const uint4*>(Q + at * 2);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                           __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+          } else {
+            copy16(smem_u32(dst), Q + at * 2, in);
           }
         }
-        if (pos < 0) return -1;
-        int off;
-        const int id = page_of(a, s.b, pos, off);
-        return id >= 0 ? id * t.row_stride_page + off * a.Hkv + s.hk : -1;
-      };
-      int next = cache_row(s.tile0);
+        if constexpr (kFp8) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.q_full[qb]);
+        } else {
+          copies_arrive(&S.q_full[qb]);
+        }
+        ++qn;
+      }
       for (int j = 0; ok && j < s.tiles; ++j) {
-        const int row = next;
-        if (j + 1 < s.tiles) next = cache_row(s.tile0 + j + 1);  // a tile ahead of its copies
+        if constexpr (kFp8)
+          if (tok * 2 < fill) post_tokens();  // the tile before: its scales have come
+        int row = -1;
+        if (b_seen) {
+          if ((unsigned)b_id < (unsigned)a.n_pages)
+            row = b_id * t.row_stride_page + b_off * a.Hkv + b_hk;
+          else
+            report_error(a.status, DSA_ERR_INVALID_ARG, 41);
+        }
+        if constexpr (kSel) tok_seen = __ballot_sync(0xffffffffu, b_seen);
+        if constexpr (kFp8) {
+          tok_ks = tok_vs = 0.f;
+          if (row >= 0) {
+            const int64_t at = ((int64_t)b_id * a.page + b_off) * a.Hkv + b_hk;
+            tok_ks = a.K_scale[at];
+            tok_vs = a.V_scale[at];
+          }
+        } else if constexpr (kSel) {
+          post_tokens();
+        }
+        look_page();
+        look_entry();
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++fill) {
           uint32_t dst;
           if constexpr (kFp8) {  // this thread has read what the stage held
-            dst = smem_u32(S.raw[fill % C::kRaw]) + tid * 16;
+            dst = smem_u32(S.raw[fill % kRaw]) + tid * 16;
           } else {
             const int r = fill % C::kSlots;
             ok = ok && mbar_wait<true>(&S.empty[r], ((fill / C::kSlots) & 1) ^ 1, abort_flag, a.status, 71, budget);
@@ -568,8 +701,8 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
           }
           if constexpr (kFp8) {
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (fill - ready >= C::kRaw - 1) {
-              asm volatile("cp.async.wait_group %0;" ::"n"(C::kRaw > 0 ? C::kRaw - 1 : 0) : "memory");
+            if (fill - ready >= kRaw - 1) {
+              asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
               convert();
               if (!ok) break;
             }
@@ -581,297 +714,517 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
     }
     // never leave with a copy in flight
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if constexpr (kFp8)
+    if constexpr (kFp8) {
+      if (ok && tok * 2 < fill) post_tokens();
       while (ok && ready < fill) convert();
+    }
   } else if (warp == kMma) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
-      constexpr uint32_t kIdescO = idesc_bf16_f32(D, N) | (1u << 15) | (1u << 16);  // A along M, B along N contiguous
-      int n = 0, qn = 0, seg_done = 0;  // tiles issued, segments begun / ended
-      bool ok = true, pending = false, pend_first = false, pend_last = false;
-      auto values = [&](int i, bool first, bool last) {  // O += V^T P^T of tile i
-        const int f = 2 * i + 1, r = f % C::kSlots, pb = i & 1;
-        if (!mbar_wait(&S.full[r], (f / C::kSlots) & 1, abort_flag, a.status, 80, budget)) return false;
-        if (!mbar_wait(&S.p_full[pb], (i >> 1) & 1, abort_flag, a.status, 81, budget)) return false;
-        if (first && seg_done > 0 &&
-            !mbar_wait(&S.o_free, (seg_done - 1) & 1, abort_flag, a.status, 82, budget))
-          return false;
-        fence_async_smem();  // the loaders' copies, before the matrix unit reads them
-        tc_fence_after();
-        const uint32_t v = smem_u32(S.ring[r]), p = smem_u32(S.p[pb]);
+    // ---------------- MMA issuer: the warp waits, one lane issues ----------------
+    constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
+    constexpr uint32_t kIdescO = C::kRows ? idesc_bf16_f32(128, D) | (1u << 16)                // V along N
+                                          : idesc_bf16_f32(D, N) | (1u << 15) | (1u << 16);  // V^T along M, P along N
+    const bool leader = elect_one();
+    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(S.ring[0])), vdesc = mnmajor_desc<128>(smem_u32(S.ring[0]), kTile * 128);
+    const uint64_t qdesc = sw128_kmajor_desc(smem_u32(S.q[0])), pdesc = mnmajor_desc<C::kPRow>(smem_u32(S.p[0]), kTile * 128);
+    int n = 0, seg = 0;  // tiles, segments
+    int slot = 0;        // ring slot of the next K tile
+    uint32_t ring_phase = 0;
+    bool ok = true, pending = false, pend_first = false, pend_last = false;
+    int pend_slot = 0, pend_seg = 0;
+    uint32_t pend_phase = 0;
+    auto values = [&](int i) {  // the output tile += weights x V of tile i
+      const int pb = i & 1, par = pend_seg % C::kOBufs;
+      ok = mbar_wait(&S.full[pend_slot], pend_phase, abort_flag, a.status, 80, budget) &&
+           mbar_wait(&S.p_full[pb], (i >> 1) & 1, abort_flag, a.status, 81, budget) &&
+           (!pend_first || pend_seg < C::kOBufs ||
+            mbar_wait(&S.o_free[par], (pend_seg / C::kOBufs - 1) & 1, abort_flag, a.status, 82, budget));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      fence_async_smem();  // the loaders' copies, before the matrix unit reads them
+      tc_fence_after();
+      if (leader) {
+        const uint64_t v = vdesc + (uint64_t)(pend_slot * (C::kSlotBytes >> 4));
+        const uint64_t p = pdesc + (uint64_t)(pb * (C::kPBytes >> 4));
+        const uint32_t o = tmem_base + C::kOCol + par * C::kOCols, ps = tmem_base + C::kPCol + pb * 64;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc_mma_bf16(tmem_base + 2 * N, mnmajor_desc<128>(v + k * 2048, kTile * 128),
-                      mnmajor_desc<C::kPRow>(p + k * 16 * C::kPRow, kTile * 128), kIdescO, !(first && k == 0));
-        tc_commit(&S.empty[r]);
-        tc_commit(&S.p_empty[pb]);
-        if (last) {
-          tc_commit(&S.o_full);
-          ++seg_done;
+        for (int k = 0; k < kTile / 16; ++k) {
+          if constexpr (C::kRows)
+            tc_mma_bf16_ts(o, ps + k * 8, v + (uint64_t)(k * (2048 >> 4)), kIdescO,
+                           !(pend_first && k == 0));
+          else
+            tc_mma_bf16(o, v + (uint64_t)(k * (2048 >> 4)), p + (uint64_t)(k * C::kPRow), kIdescO,
+                        !(pend_first && k == 0));
         }
-        return true;
-      };
-      while (ok && walk.next(t, s)) {
-        if (!s.valid) continue;
-        const int qb = qn % C::kQBufs;
-        if (!(ok = mbar_wait(&S.q_full[qb], (qn / C::kQBufs) & 1, abort_flag, a.status, 83, budget))) break;
-        const uint32_t q = smem_u32(S.q[qb]);
-        for (int j = 0; j < s.tiles; ++j, ++n) {
-          const int f = 2 * n, r = f % C::kSlots, sb = n & 1;
-          if (!(ok = mbar_wait(&S.full[r], (f / C::kSlots) & 1, abort_flag, a.status, 84, budget))) break;
-          if (!(ok = mbar_wait(&S.s_empty[sb], ((n >> 1) & 1) ^ 1, abort_flag, a.status, 85, budget))) break;
-          fence_async_smem();
-          tc_fence_after();
-          const uint32_t k = smem_u32(S.ring[r]);
+        tc_commit(&S.empty[pend_slot]);
+        tc_commit(&S.p_empty[pb]);
+        if (pend_last) tc_commit(&S.o_full[par]);
+      }
+      __syncwarp();
+    };
+    auto step = [&]() {
+      if (++slot == C::kSlots) {
+        slot = 0;
+        ring_phase ^= 1;
+      }
+    };
+    while (ok && walk.next(t, s)) {
+      if (!s.valid) continue;
+      const int qb = seg % C::kQBufs;
+      ok = mbar_wait(&S.q_full[qb], (seg / C::kQBufs) & 1, abort_flag, a.status, 83, budget);
+      ok = __all_sync(0xffffffffu, ok);
+      for (int j = 0; ok && j < s.tiles; ++j, ++n) {
+        ok = mbar_wait(&S.full[slot], ring_phase, abort_flag, a.status, 84, budget);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // the score tile is free: the weights of tile n - 2 were waited for below
+        fence_async_smem();
+        tc_fence_after();
+        if (leader) {
+          const uint64_t k = kdesc + (uint64_t)(slot * (C::kSlotBytes >> 4));
+          const uint64_t q = qdesc + (uint64_t)(qb * (C::kQBytes >> 4));
+          const uint32_t d = tmem_base + (n & 1) * C::kSCols;
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16(tmem_base + sb * N, sw128_kmajor_desc(k + c * kTile * 128 + kk * 32),
-                          sw128_kmajor_desc(q + c * N * 128 + kk * 32), kIdescS, (c | kk) != 0);
-          tc_commit(&S.empty[r]);
-          tc_commit(&S.s_full[sb]);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ko = k + (uint64_t)((c * kTile * 128 + kk * 32) >> 4);
+              const uint64_t qo = q + (uint64_t)((c * N * 128 + kk * 32) >> 4);
+              tc_mma_bf16(d, C::kRows ? qo : ko, C::kRows ? ko : qo, kIdescS, (c | kk) != 0);
+            }
+          tc_commit(&S.empty[slot]);
+          tc_commit(&S.s_full[n & 1]);
           if (j == s.tiles - 1) tc_commit(&S.q_empty[qb]);
-          if (pending && !(ok = values(n - 1, pend_first, pend_last))) break;
-          pending = true;
-          pend_first = j == 0;
-          pend_last = j == s.tiles - 1;
         }
-        ++qn;
+        __syncwarp();
+        step();
+        if (pending) values(n - 1);
+        pending = true;
+        pend_first = j == 0;
+        pend_last = j == s.tiles - 1;
+        pend_seg = seg;
+        pend_slot = slot;
+        pend_phase = ring_phase;
+        step();
       }
-      if (ok && pending) values(n - 1, pend_first, pend_last);
-      // never leave with an MMA in flight
+      ++seg;
+    }
+    if (ok && pending) values(n - 1);
+    // never leave with an MMA in flight
+    if (leader) {
       tc_commit(&S.drain);
       mbar_wait_drain(&S.drain, 0, a.status, 86);
     }
-  } else if (warp < kSoftWarps) {
+    __syncwarp();
+  } else {
     // ---------------- softmax ----------------
-    constexpr int kC = N / 2, kStep = kC > 32 ? 32 : kC;  // columns of a warp, of one TMEM load
-    const int wg = warp >> 2, wq = warp & 3, tid = threadIdx.x & 127, bar = 1 + wg;
-    const int key = wq * 32 + lane, c0 = wg * kC;
+    const int wg = warp >> 2, wq = warp & 3, tid = threadIdx.x & 127;
+    constexpr int kGroup = C::kRows ? 256 : 128;
+    const int bar = C::kRows ? 1 : 1 + wg;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const float c2 = a.scale * 1.44269504f;  // scores in powers of two
-    // this thread's P row: 64 columns a chunk, 16-byte units swizzled over the row's width
-    const uint32_t p_off = (uint32_t)((N == 128 ? wg * kTile * 128 : 0) + key * C::kPRow);
-    const uint32_t p_unit = N == 128 ? 0 : wg * (kC / 8);
-    const uint32_t p_sw = C::kPRow == 128 ? key & 7 : (C::kPRow == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
-    int n = 0, seg = 0, first_seg = 1;
-    bool ok = true;
-    while (walk.next(t, s)) {
-      if (!s.valid) {
-        first_seg = 0;
-        continue;
-      }
-      if (tid < kC) {
-        const int r = c0 + tid, rr = s.row0 + r, j = rr / g;
-        S.mref[r] = kNoMax;
-        S.lim[r] = kSel ? 0 : s.lim0 + j;
-        S.orow[r] = r < s.rows ? (s.q0 + j) * a.Hq + s.hk * g + (rr - j * g) : -1;
-      }
-      named_bar(bar, 128);
-      float l[kC];
-#pragma unroll
-      for (int i = 0; i < kC; ++i) l[i] = 0.f;
-      // what this thread's token of the next tile needs beside its scores
-      bool seen_next = true;
-      float ks_next = 1.f, vs_next = 1.f;
-      auto token = [&](int tile) {
-        const int e = tile * kTile + key;
-        int pos = e < s.end ? e : -1;
-        if constexpr (kSel) {
-          if (pos >= 0) {
-            pos = a.idx[(int64_t)s.q0 * a.k + e];
-            if (pos > s.lim0) pos = -1;
-          }
-        }
-        seen_next = pos >= 0;
-        if constexpr (kFp8) {
-          ks_next = 0.f;
-          vs_next = 0.f;
-          if (pos >= 0) {
-            int off;
-            const int id = page_of(a, s.b, pos, off);
-            if (id >= 0) {
-              const int64_t at = ((int64_t)id * a.page + off) * a.Hkv + s.hk;
-              ks_next = a.K_scale[at];
-              vs_next = a.V_scale[at];
-            }
-          }
-        }
-      };
-      if constexpr (kSel || kFp8) token(s.tile0);
-      for (int j = 0; j < s.tiles; ++j, ++n) {
-        const int sb = n & 1, tile = s.tile0 + j;
-        const float cs = kFp8 ? c2 * ks_next : c2, vs = vs_next;
-        const bool seen = seen_next;
-        if constexpr (kSel || kFp8)
-          if (j + 1 < s.tiles) token(tile + 1);
-        const int pos = tile * kTile + key;
-        // some row does not see some token of this tile
-        const bool masked = kSel || (tile + 1) * kTile > s.lim0 + 1;
-        ok = ok && mbar_wait(&S.s_full[sb], (n >> 1) & 1, abort_flag, a.status, 90, budget);
+    int n = 0, seg = 0;
+    bool ok = true, first_seg = true;
+    // the segment before, whose output tile is stored behind the next one's first tile
+    bool pend = false, pend_whole = false;
+    int pend_par = 0, pend_phase = 0;
+    int64_t pend_part = 0;
+    // e4m3: the converted V's columns come in the order 0, 2, 1, 3 of every four
+    auto element = [](int c) { return kFp8 ? ((c & ~3) | ((c & 1) << 1) | ((c >> 1) & 1)) : c; };
+
+    if constexpr (C::kRows) {
+      // A thread owns one query row and half of the tile's tokens.
+      const int r = tid, c0 = wg * 64;
+      float pend_inv = 0.f;
+      int pend_row = -1;
+      auto store_output = [&]() {
+        if (!pend) return;
+        pend = false;
+        ok = ok && mbar_wait(&S.o_full[pend_par], pend_phase, abort_flag, a.status, 93, budget);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        const uint32_t col = tmem_base + lanes + (uint32_t)(sb * N + c0);
-        float x[kStep];
-        auto scores = [&](int i0) {  // x = log2 weights against the reference
-          tmem_ld<kStep>(col + i0, x);
-          tmem_ld_wait();
+        constexpr int kHalf = D / 2;
+        const uint32_t o = tmem_base + lanes + (uint32_t)(C::kOCol + pend_par * C::kOCols + wg * kHalf);
 #pragma unroll
-          for (int i = 0; i < kStep; ++i) {
-            float v = x[i];
-            if (masked) {
-              const bool vis = kSel ? seen : pos <= S.lim[c0 + i0 + i];
-              v = vis ? v * cs : -INFINITY;
-              x[i] = v - S.mref[c0 + i0 + i];
-            } else {
-              x[i] = fmaf(v, cs, -S.mref[c0 + i0 + i]);
+        for (int i0 = 0; i0 < kHalf; i0 += 32) {
+          float v[32];
+          tmem_ld<32>(o + i0, v);
+          tmem_ld_wait();
+          if (!ok) continue;
+          const int c = wg * kHalf + i0;
+          if (!pend_whole) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + (pend_part * N + r) * D + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) dst[i >> 2] = kFp8 ? make_float4(v[i], v[i + 2], v[i + 1], v[i + 3]) : make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          } else if (pend_row >= 0) {
+            uint8_t* dst = static_cast<uint8_t*>(a.out) + ((int64_t)pend_row * a.d + c) * 2;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 8; e += 2)
+                w[e >> 1] = pack_bf16(v[element(i + e)] * pend_inv, v[element(i + e + 1)] * pend_inv);
+              if (c + i < a.d) *reinterpret_cast<uint4*>(dst + i * 2) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-        };
-        float top = -INFINITY;
-#pragma unroll
-        for (int i0 = 0; i0 < kC; i0 += kStep) {
-          scores(i0);
-#pragma unroll
-          for (int i = 0; i < kStep; ++i) top = fmaxf(top, x[i]);
         }
-        if (bar_or(bar, 128, top > kSlack || !ok)) {
-          if (bar_or(bar, 128, !ok)) {
-            ok = false;
-            break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.o_free[pend_par]);
+      };
+      while (walk.next(t, s)) {
+        if (!s.valid) {
+          first_seg = false;
+          continue;
+        }
+        const int rr = s.row0 + r, jq = rr / g;
+        const int orow = r < s.rows ? (s.q0 + jq) * a.Hq + s.hk * g + (rr - jq * g) : -1;
+        const int lim = kSel ? 0x7fffffff : s.lim0 + jq;
+        float nref = -kNoMax, l = 0.f;
+        for (int j = 0; j < s.tiles; ++j, ++n) {
+          const int tile = s.tile0 + j, tk = n % kTok;
+          if constexpr (kSel || kFp8) ok = ok && mbar_wait(&S.tok_full[tk], (n / kTok) & 1, abort_flag, a.status, 94, budget);
+          ok = ok && mbar_wait(&S.s_full[n & 1], (n >> 1) & 1, abort_flag, a.status, 90, budget);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          const uint32_t col = tmem_base + lanes + (uint32_t)((n & 1) * C::kSCols + c0);
+          uint32_t seen[2] = {0xffffffffu, 0xffffffffu};
+          bool masked;
+          if constexpr (kSel) {
+            seen[0] = S.seen[tk][wg * 2];
+            seen[1] = S.seen[tk][wg * 2 + 1];
+            masked = (seen[0] & seen[1]) != 0xffffffffu;
+          } else {
+            masked = (tile + 1) * kTile > s.lim0 + 1;  // some row does not see some token of this tile
+            if (masked) {
+              const int left = lim - tile * kTile - c0 + 1;  // tokens of this half that the row sees
+              seen[0] = left >= 32 ? 0xffffffffu : (left <= 0 ? 0u : (1u << left) - 1);
+              seen[1] = left >= 64 ? 0xffffffffu : (left <= 32 ? 0u : (1u << (left - 32)) - 1);
+            }
           }
-          // new references: the rows' maxima so far
-#pragma unroll
-          for (int i0 = 0; i0 < kC; i0 += kStep) {
-            if (kC > kStep) scores(i0);
-            // back to plain scores: the reference may be far off (none yet)
-            tmem_ld<kStep>(col + i0, x);
+          float x[64];
+          auto scores = [&](float ref) {  // log2 weights against the reference -ref
+            tmem_ld<32>(col, *reinterpret_cast<float(*)[32]>(x));
+            tmem_ld<32>(col + 32, *reinterpret_cast<float(*)[32]>(x + 32));
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < kStep; ++i) {
-              const bool vis = !masked || (kSel ? seen : pos <= S.lim[c0 + i0 + i]);
-              x[i] = vis ? x[i] * cs : -INFINITY;
+            for (int i = 0; i < 64; i += 4) {
+              float4 k = make_float4(c2, c2, c2, c2);
+              if constexpr (kFp8) k = *reinterpret_cast<const float4*>(&S.ksc[tk][c0 + i]);
+              const float2 u = fma2(make_float2(x[i], x[i + 1]), make_float2(k.x, k.y), make_float2(ref, ref));
+              const float2 v = fma2(make_float2(x[i + 2], x[i + 3]), make_float2(k.z, k.w), make_float2(ref, ref));
+              x[i] = u.x;
+              x[i + 1] = u.y;
+              x[i + 2] = v.x;
+              x[i + 3] = v.y;
             }
-            const float m = warp_columns<kStep, true>(x);
-            if (lane < kStep) S.red[wg][wq][i0 + lane] = m;
-          }
-          named_bar(bar, 128);
-          if (tid < kC) {
-            const float old = S.mref[c0 + tid];
-            float m = old;
+            if (masked) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) m = fmaxf(m, S.red[wg][w][tid]);
-            S.mref[c0 + tid] = m;
-            S.fac[c0 + tid] = ex2(old - m);
-          }
-          named_bar(bar, 128);
-#pragma unroll
-          for (int i = 0; i < kC; ++i) l[i] *= S.fac[c0 + i];
-          if (j > 0) {  // O holds the tiles before: wait for the last of them, then scale
-            ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 91, budget);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
-            const uint32_t o = tmem_base + lanes + (uint32_t)(2 * N + c0);
-#pragma unroll
-            for (int i0 = 0; i0 < kC; i0 += 8) {
-              float v[8];
-              tmem_ld<8>(o + i0, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] *= S.fac[c0 + i0 + i];
-              tmem_st8(o + i0, v);
+              for (int i = 0; i < 64; ++i)
+                if (!((seen[i >> 5] >> (i & 31)) & 1)) x[i] = -INFINITY;
             }
-            tmem_st_wait();
+          };
+          auto highest = [&]() {
+            float m0 = x[0], m1 = x[1];
+#pragma unroll
+            for (int i = 2; i < 64; i += 4) {
+              m0 = fmaxf(fmaxf(m0, x[i]), x[i + 1]);
+              if (i + 3 < 64) m1 = fmaxf(fmaxf(m1, x[i + 2]), x[i + 3]);
+            }
+            return fmaxf(m0, m1);
+          };
+          scores(nref);
+          if (bar_or(bar, kGroup, highest() > kSlack || !ok)) {
+            if (bar_or(bar, kGroup, !ok)) {
+              ok = false;
+              break;
+            }
+            // new references: the rows' maxima so far, from the plain scores (the old reference may be far off, or none)
+            scores(0.f);
+            (&S.red[0][0][0])[wg * 128 + r] = highest();
+            named_bar(bar, kGroup);
+            const float m = fmaxf(-nref, fmaxf((&S.red[0][0][0])[r], (&S.red[0][0][0])[128 + r]));
+            const float fac = ex2(-nref - m);
+            nref = -m;
+            l *= fac;
+            if (j > 0) {  // the output tile holds the tiles before: wait for the last of them, then scale
+              ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 91, budget);
+              ok = __all_sync(0xffffffffu, ok);
+              tc_fence_after();
+              const uint32_t o = tmem_base + lanes + (uint32_t)(C::kOCol + (seg % C::kOBufs) * C::kOCols + wg * (D / 2));
+#pragma unroll
+              for (int i0 = 0; i0 < D / 2; i0 += 8) {
+                float v[8];
+                uint32_t w[8];
+                tmem_ld<8>(o + i0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i] * fac);
+                tmem_st8(o + i0, w);
+              }
+              tmem_st_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] += nref;
           }
-          if constexpr (kC == kStep) scores(0);
+          // the weights' tile is free: the scores just read were multiplied after the weights of tile n - 2
+          const uint32_t pcol = tmem_base + lanes + (uint32_t)(C::kPCol + (n & 1) * 64 + wg * 32);
+          float2 l2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i0 = 0; i0 < 64; i0 += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              float2 u = make_float2(ex2(x[i0 + i]), ex2(x[i0 + i + 1])), v = make_float2(ex2(x[i0 + i + 2]), ex2(x[i0 + i + 3]));
+              l2 = add2(l2, add2(u, v));
+              if constexpr (kFp8) {
+                const float4 vs = *reinterpret_cast<const float4*>(&S.vsc[tk][c0 + i0 + i]);
+                u.x *= vs.x;
+                u.y *= vs.y;
+                v.x *= vs.z;
+                v.y *= vs.w;
+              }
+              w[i >> 1] = pack_bf16(u.x, u.y);
+              w[(i >> 1) + 1] = pack_bf16(v.x, v.y);
+            }
+            tmem_st8(pcol + (i0 >> 1), w);
+          }
+          l += l2.x + l2.y;
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.p_full[n & 1]);
+          if (j == 0) store_output();
         }
-        // P(n - 2) has been read
-        if (n >= 2) ok = ok && mbar_wait(&S.p_empty[sb], ((n >> 1) & 1) ^ 1, abort_flag, a.status, 92, budget);
+        // ---- the segment's sums ----
+        if (bar_or(bar, kGroup, !ok)) {
+          ok = false;
+          break;
+        }
+        (&S.red[0][0][0])[wg * 128 + r] = l;
+        named_bar(bar, kGroup);
+        const float sum = (&S.red[0][0][0])[r] + (&S.red[0][0][0])[128 + r];
+        pend = true;
+        pend_whole = s.tiles == s.unit_tiles;
+        pend_part = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
+        pend_par = seg % C::kOBufs;
+        pend_phase = (seg / C::kOBufs) & 1;
+        pend_row = orow;
+        pend_inv = sum > 0.f ? 1.f / sum : 0.f;
+        if (wg == 0) {
+          if (!pend_whole) {
+            a.part_ml[(pend_part * N + r) * 2] = -nref;
+            a.part_ml[(pend_part * N + r) * 2 + 1] = sum;
+          } else if (a.lse != nullptr && orow >= 0) {
+            a.lse[orow] = sum > 0.f ? (log2f(sum) - nref) * 0.693147181f : -INFINITY;
+          }
+        }
+        ++seg;
+        first_seg = false;
+      }
+      if (ok) store_output();
+    } else {
+      // A thread owns one token and half of the query rows.
+      constexpr int kC = N / 2;
+      const int key = wq * 32 + lane, c0 = wg * kC;
+      // this thread's P row: 16-byte units swizzled over the row's width
+      const uint32_t p_off = (uint32_t)(key * C::kPRow), p_unit = wg * (kC / 8);
+      const uint32_t p_sw = C::kPRow == 128 ? key & 7 : (C::kPRow == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
+      // 128 rows of O^T fill the 128 lanes; 64 fill the first 16 lanes of each warp
+      const int dv = element(D == 128 ? wq * 32 + lane : wq * 16 + lane);
+      const bool dv_ok = (D == 128 || lane < 16);
+      auto store_output = [&]() {
+        if (!pend) return;
+        pend = false;
+        ok = ok && mbar_wait(&S.o_full[pend_par], pend_phase, abort_flag, a.status, 93, budget);
         ok = __all_sync(0xffffffffu, ok);
-        uint8_t* prow = S.p[sb] + p_off;
+        tc_fence_after();
+        const uint32_t o = tmem_base + lanes + (uint32_t)(C::kOCol + pend_par * C::kOCols + c0);
+        float v[kC];
+        tmem_ld<kC>(o, v);
+        tmem_ld_wait();
+        if (ok && dv_ok) {
+          if (!pend_whole) {
+            float* dst = a.part_o + (pend_part * N + c0) * D + dv;
 #pragma unroll
-        for (int i0 = 0; i0 < kC; i0 += kStep) {
-          if (kC > kStep) scores(i0);
+            for (int i = 0; i < kC; ++i) dst[i * D] = v[i];
+          } else if (dv < a.d) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + dv;
 #pragma unroll
-          for (int i = 0; i < kStep; i += 8) {
+            for (int i = 0; i < kC; ++i) {
+              const int r = S.orow[pend_par][c0 + i];
+              if (r >= 0) out[(int64_t)r * a.d] = __float2bfloat16_rn(v[i] * S.lsum[pend_par][c0 + i]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.o_free[pend_par]);
+      };
+      while (walk.next(t, s)) {
+        if (!s.valid) {
+          first_seg = false;
+          continue;
+        }
+        if (tid < kC) {
+          const int r = c0 + tid, rr = s.row0 + r, j = rr / g;
+          S.nref[r] = -kNoMax;
+          S.lim[r] = kSel ? 0 : s.lim0 + j;
+          S.orow[seg & 1][r] = r < s.rows ? (s.q0 + j) * a.Hq + s.hk * g + (rr - j * g) : -1;
+        }
+        named_bar(bar, 128);
+        float2 l[kC / 2];
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) l[i] = make_float2(0.f, 0.f);
+        for (int j = 0; j < s.tiles; ++j, ++n) {
+          const int tile = s.tile0 + j, tk = n % kTok;
+          if constexpr (kSel || kFp8) ok = ok && mbar_wait(&S.tok_full[tk], (n / kTok) & 1, abort_flag, a.status, 94, budget);
+          ok = ok && mbar_wait(&S.s_full[n & 1], (n >> 1) & 1, abort_flag, a.status, 90, budget);
+          ok = __all_sync(0xffffffffu, ok);
+          tc_fence_after();
+          const uint32_t col = tmem_base + lanes + (uint32_t)((n & 1) * C::kSCols + c0);
+          const int pos = tile * kTile + key;
+          bool masked, seen = true;
+          if constexpr (kSel) {
+            const uint32_t all = S.seen[tk][wq];
+            masked = all != 0xffffffffu;
+            seen = (all >> lane) & 1;
+          } else {
+            masked = (tile + 1) * kTile > s.lim0 + 1;  // some row does not see some token of this tile
+          }
+          const float cs = kFp8 ? S.ksc[tk][kFp8 ? key : 0] : c2;
+          float x[kC];
+          auto hide = [&]() {
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < kC; ++i)
+                if (!(kSel ? seen : pos <= S.lim[c0 + i])) x[i] = -INFINITY;
+            }
+          };
+          auto scores = [&]() {  // log2 weights against the references
+            tmem_ld<kC>(col, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < kC; i += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(&S.nref[c0 + i]);
+              const float2 u = fma2(make_float2(x[i], x[i + 1]), make_float2(cs, cs), make_float2(m.x, m.y));
+              const float2 v = fma2(make_float2(x[i + 2], x[i + 3]), make_float2(cs, cs), make_float2(m.z, m.w));
+              x[i] = u.x;
+              x[i + 1] = u.y;
+              x[i + 2] = v.x;
+              x[i + 3] = v.y;
+            }
+            hide();
+          };
+          scores();
+          float top = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int i = 2; i < kC; i += 2) top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
+          if (bar_or(bar, 128, top > kSlack || !ok)) {
+            if (bar_or(bar, 128, !ok)) {
+              ok = false;
+              break;
+            }
+            // new references: the rows' maxima so far, from the plain scores (the old reference may be far off, or none)
+            tmem_ld<kC>(col, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < kC; ++i) x[i] *= cs;
+            hide();
+            const float m = warp_columns<kC, true>(x);
+            if (lane < kC) S.red[wg][wq][lane] = m;
+            named_bar(bar, 128);
+            if (tid < kC) {
+              const float old = -S.nref[c0 + tid];
+              float mm = old;
+#pragma unroll
+              for (int w = 0; w < 4; ++w) mm = fmaxf(mm, S.red[wg][w][tid]);
+              S.nref[c0 + tid] = -mm;
+              S.fac[c0 + tid] = ex2(old - mm);
+            }
+            named_bar(bar, 128);
+#pragma unroll
+            for (int i = 0; i < kC / 2; ++i) {
+              l[i].x *= S.fac[c0 + 2 * i];
+              l[i].y *= S.fac[c0 + 2 * i + 1];
+            }
+            if (j > 0) {  // the output tile holds the tiles before: wait for the last of them, then scale
+              ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 91, budget);
+              ok = __all_sync(0xffffffffu, ok);
+              tc_fence_after();
+              const uint32_t o = tmem_base + lanes + (uint32_t)(C::kOCol + (seg & 1) * C::kOCols + c0);
+#pragma unroll
+              for (int i0 = 0; i0 < kC; i0 += 8) {
+                float v[8];
+                uint32_t w[8];
+                tmem_ld<8>(o + i0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i] * S.fac[c0 + i0 + i]);
+                tmem_st8(o + i0, w);
+              }
+              tmem_st_wait();
+            }
+            scores();
+          }
+          // P's buffer is free: the scores just read were multiplied after the weights of tile n - 2
+          uint8_t* prow = S.p[n & 1] + p_off;
+          const float vs = kFp8 ? S.vsc[tk][kFp8 ? key : 0] : 1.f;
+#pragma unroll
+          for (int i = 0; i < kC; i += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-              const float w0 = ex2(x[i + e]), w1 = ex2(x[i + e + 1]);
-              l[i0 + i + e] += w0;
-              l[i0 + i + e + 1] += w1;
-              const __nv_bfloat162 b = kFp8 ? __floats2bfloat162_rn(w0 * vs, w1 * vs) : __floats2bfloat162_rn(w0, w1);
-              w[e >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+              const float2 u = make_float2(ex2(x[i + e]), ex2(x[i + e + 1]));
+              l[(i + e) >> 1] = add2(l[(i + e) >> 1], u);
+              w[e >> 1] = kFp8 ? pack_bf16(u.x * vs, u.y * vs) : pack_bf16(u.x, u.y);
             }
-            *reinterpret_cast<uint4*>(prow + (((p_unit + ((i0 + i) >> 3)) ^ p_sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(prow + (((p_unit + (i >> 3)) ^ p_sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          fence_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.p_full[n & 1]);
+          if (j == 0) store_output();
         }
-        fence_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.s_empty[sb]);
-          mbar_arrive(&S.p_full[sb]);
+        // ---- the segment's sums ----
+        if (bar_or(bar, 128, !ok)) {
+          ok = false;
+          break;
         }
-      }
-      // ---- the segment's sums ----
-      if (bar_or(bar, 128, !ok)) break;
+        pend = true;
+        pend_whole = s.tiles == s.unit_tiles;
+        pend_part = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
+        pend_par = seg & 1;
+        pend_phase = (seg >> 1) & 1;
+        {
+          float v[kC];
 #pragma unroll
-      for (int i0 = 0; i0 < kC; i0 += kStep) {
-        float v[kStep];
-#pragma unroll
-        for (int i = 0; i < kStep; ++i) v[i] = l[i0 + i];
-        const float sum = warp_columns<kStep, false>(v);
-        if (lane < kStep) S.red[wg][wq][i0 + lane] = sum;
-      }
-      named_bar(bar, 128);
-      const bool whole = s.tiles == s.unit_tiles;
-      const int64_t part = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
-      if (tid < kC) {
-        const int r = c0 + tid;
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += S.red[wg][w][tid];
-        if (whole) {
-          if (a.lse != nullptr && S.orow[r] >= 0)
-            a.lse[S.orow[r]] = sum > 0.f ? (S.mref[r] + log2f(sum)) * 0.693147181f : -INFINITY;
-          S.lsum[r] = sum > 0.f ? 1.f / sum : 0.f;
-        } else {
-          a.part_ml[(part * N + r) * 2] = S.mref[r];
-          a.part_ml[(part * N + r) * 2 + 1] = sum;
+          for (int i = 0; i < kC / 2; ++i) {
+            v[2 * i] = l[i].x;
+            v[2 * i + 1] = l[i].y;
+          }
+          const float sum = warp_columns<kC, false>(v);
+          if (lane < kC) S.red[wg][wq][lane] = sum;
         }
-      }
-      named_bar(bar, 128);
-      ok = ok && mbar_wait(&S.o_full, seg & 1, abort_flag, a.status, 93, budget);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-      // 128 rows of O^T fill the 128 lanes; 64 fill the first 16 lanes of each warp
-      const int dv = D == 128 ? wq * 32 + lane : wq * 16 + lane;
-      const bool mine = D == 128 || lane < 16;
-      const uint32_t o = tmem_base + lanes + (uint32_t)(2 * N + c0);
+        named_bar(bar, 128);
+        if (tid < kC) {
+          const int r = c0 + tid;
+          float sum = 0.f;
 #pragma unroll
-      for (int i0 = 0; i0 < kC; i0 += 8) {
-        float v[8];
-        tmem_ld<8>(o + i0, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = c0 + i0 + i;
-          if (!mine || !ok) continue;
-          if (!whole)
-            a.part_o[(part * N + r) * D + dv] = v[i];
-          else if (S.orow[r] >= 0 && dv < a.d)
-            static_cast<__nv_bfloat16*>(a.out)[(int64_t)S.orow[r] * a.d + dv] = __float2bfloat16_rn(v[i] * S.lsum[r]);
+          for (int w = 0; w < 4; ++w) sum += S.red[wg][w][tid];
+          if (!pend_whole) {
+            a.part_ml[(pend_part * N + r) * 2] = -S.nref[r];
+            a.part_ml[(pend_part * N + r) * 2 + 1] = sum;
+          } else if (a.lse != nullptr && S.orow[pend_par][r] >= 0) {
+            a.lse[S.orow[pend_par][r]] = sum > 0.f ? (log2f(sum) - S.nref[r]) * 0.693147181f : -INFINITY;
+          }
+          S.lsum[pend_par][r] = sum > 0.f ? 1.f / sum : 0.f;
         }
+        named_bar(bar, 128);  // the rows' state is free for the next segment
+        ++seg;
+        first_seg = false;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.o_free);
-      named_bar(bar, 128);  // the rows' state is free for the next segment
-      ++seg;
-      first_seg = 0;
+      if (ok) store_output();
     }
   }
 
