@@ -12,13 +12,17 @@
 // flops a byte, and at N <= 128 memory is the bound.
 //
 // One persistent CTA per SM:
-//   * four loader warps turn positions into cache rows (page table, or list
-//     entry and page table; a thread looks up one token, a tile ahead) and
-//     fetch them by 16-byte asynchronous copies into a ring that K and V tiles
-//     share, whatever the page size; a token that no row sees, and the columns
+//   * three lookup warps turn positions into cache rows (page table, or list
+//     entry and page table), post them with the tokens' masks and scales a
+//     few tiles ahead, and fetch the queries;
+//   * sixteen copy warps, eight for K and eight for V, fetch the rows by
+//     16-byte asynchronous copies into a ring that K and V tiles share,
+//     whatever the page size; a token that no row sees, and the columns
 //     behind d, are filled with zeros, so no stale value meets a zero weight.
-//     e4m3 rows land in a staging ring of which each thread reads back, once
-//     they are there, the bytes it asked for, and writes them as bf16 (exact);
+//     One warp issues such a copy of scattered rows every 60 cycles or so:
+//     sixteen reach 17 TB/s from L2 and 7 TB/s from memory, eight 14.5 and
+//     5.7, four 8.7 and 3.3.  e4m3 rows come through registers, a tile ahead,
+//     and are written as bf16 (exact);
 //   * the MMA warp issues S(t+1) before O(t), so that the tensor pipe has
 //     work while the softmax of a tile runs;
 //   * eight softmax warps: four cover the 128 tokens for the first N/2 rows,
@@ -44,8 +48,8 @@
 namespace dsa {
 
 constexpr int kTile = 128;           // tokens a tile
-constexpr int kSoftWarps = 8;
-constexpr int kLoadWarps = 4;
+constexpr int kSoftWarps = 8, kLookWarps = 3, kCopyWarps = 16;
+constexpr int kWarps = kSoftWarps + 1 + kLookWarps + kCopyWarps;
 constexpr float kNoMax = -1.7e38f;   // reference of a row that has seen no token
 constexpr float kSlack = 8.f;        // log2 of the largest weight
 
@@ -308,6 +312,16 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&e), *reinterpret_cast<const uint32_t*>(&o));
 }
 
+// Sets the registers of a thread of this warpgroup; the launch's total must
+// hold the sum of all shares.
+template <int kRegs, bool kMore>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (kMore)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // True in one lane of a converged warp, always the same one; the compiler
 // knows that the branch is uniform, which tcgen05 operands profit from.
 __device__ __forceinline__ bool elect_one() {
@@ -367,6 +381,7 @@ __device__ __forceinline__ float warp_columns(float (&v)[C]) {
 // ----------------------------------------------------------------------------
 // shared memory
 // ----------------------------------------------------------------------------
+constexpr int kEnd = -2;  // in place of the first row: no more tiles
 constexpr int kTok = 8;  // tiles whose token masks and scales are kept: more than the ring can run ahead
 
 template <int N, int D, bool kFp8>
@@ -374,17 +389,19 @@ struct Cfg {
   static constexpr bool kRows = N == 128;            // query rows, not tokens, on the 128 lanes
   static constexpr int kChunks = D / 64;
   static constexpr int kSlotBytes = kTile * D * 2;   // one K or V tile, bf16
-  static constexpr int kRawBytes = kTile * D;        // one e4m3 tile
   static constexpr int kQBytes = N * D * 2;
-  static constexpr int kQBufs = kRows ? 1 : 2;
+  static constexpr int kQBufs = 2;
   static constexpr int kPBytes = kRows ? 0 : N * kTile * 2;
   static constexpr int kPRow = N >= 64 ? 128 : N * 2;  // bytes of a P row
-  static constexpr int kRaw = kFp8 ? (N == 64 && D == 128 ? 3 : 4) : 0;
-  static constexpr int kOther = kQBufs * kQBytes + 2 * kPBytes + kRaw * kRawBytes + (kFp8 ? kTok * kTile * 8 : 0);
-  static constexpr int kBudget = 232448 - 1024 - 6144;
+  static constexpr int kOther = kQBufs * kQBytes + 2 * kPBytes + (kFp8 ? kTok * kTile * 8 : 0);
+  static constexpr int kBudget = 232448 - 1024 - 10240;
   static constexpr int kFit = (kBudget - kOther) / kSlotBytes;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
-  static constexpr int kWarps = kSoftWarps + 1 + kLoadWarps;
+  // Registers a thread: launched with 72 (28 warps), of which the copy warps
+  // give some up, so that the softmax warps hold a row's or token's scores.
+  // 256 x kSoftRegs + 128 x kMidRegs + 512 x kCopyRegs <= 896 x 72.
+  static constexpr int kSoftRegs = 128, kMidRegs = kFp8 ? 56 : 72, kCopyRegs = kFp8 ? 48 : 40;
+  static_assert(256 * kSoftRegs + 128 * kMidRegs + 512 * kCopyRegs <= kWarps * 32 * 72, "the registers of the launch");
   // tensor memory: two score tiles, with rows on the lanes two tiles of bf16
   // weights, and two output tiles (one where no more fit)
   static constexpr int kSCols = N, kPCol = 2 * N, kOCol = kRows ? 2 * N + 128 : 2 * N, kOCols = kRows ? D : N;
@@ -399,13 +416,13 @@ struct AttendSmem {
   uint8_t ring[C::kSlots][C::kSlotBytes];
   uint8_t q[C::kQBufs][C::kQBytes];
   uint8_t p[2][C::kPBytes ? C::kPBytes : 16];
-  uint8_t raw[C::kRaw ? C::kRaw : 1][C::kRaw ? C::kRawBytes : 16];
   float ksc[kTok][kFp8 ? kTile : 4], vsc[kTok][kFp8 ? kTile : 4];
+  int rows[kTok][kTile];
   uint32_t seen[kTok][4];
   uint64_t full[C::kSlots], empty[C::kSlots];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2], p_empty[2];
-  uint64_t o_full[2], o_free[2], tok_full[kTok], drain;
+  uint64_t o_full[2], o_free[2], tok_full[kTok], tok_empty[kTok], drain;
   float red[2][4][N / 2 > 32 ? 32 : N / 2];
   alignas(16) float nref[N];
   float fac[N], lsum[2][N];
@@ -421,7 +438,7 @@ struct AttendSmem {
 // the kernel
 // ----------------------------------------------------------------------------
 template <int N, int D, bool kFp8, bool kSel>
-__global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
+__global__ void __launch_bounds__(kWarps * 32, 1)
     attend_tc_kernel(const __grid_constant__ TcAttend t) {
   using C = Cfg<N, D, kFp8>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -435,11 +452,11 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&S.full[i], kFp8 ? kLoadWarps : kLoadWarps * 32);
+      mbar_init(&S.full[i], kCopyWarps / 2 * (kFp8 ? 1 : 32));
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.q_full[i], kFp8 ? kLoadWarps : kLoadWarps * 32);
+      mbar_init(&S.q_full[i], kLookWarps * (kFp8 ? 1 : 32));
       mbar_init(&S.q_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_full[i], kSoftWarps);
@@ -447,7 +464,10 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.o_free[i], kSoftWarps);
     }
-    for (int i = 0; i < kTok; ++i) mbar_init(&S.tok_full[i], kLoadWarps);
+    for (int i = 0; i < kTok; ++i) {
+      mbar_init(&S.tok_full[i], 1);
+      mbar_init(&S.tok_empty[i], kCopyWarps + (kSel || kFp8 ? kSoftWarps : 0));
+    }
     mbar_init(&S.drain, 1);
     S.abort_flag = 0;
     S.begin_b = 0;
@@ -467,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
   } else {
     // each thread sums a contiguous share of the requests; a block scan; the
     // thread whose share holds the run's first tile names request and offset
-    const int threads = C::kWarps * 32, share = (a.B + threads - 1) / threads;
+    const int threads = kWarps * 32, share = (a.B + threads - 1) / threads;
     const int b0 = min(a.B, (int)threadIdx.x * share), b1 = min(a.B, b0 + share);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += request_tiles<N>(a, b);
@@ -480,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
     if (lane == 31) S.sums[warp] = inc;
     __syncthreads();
     int64_t before = inc - mine, total = 0;
-    for (int w = 0; w < C::kWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += S.sums[w];
       total += S.sums[w];
     }
@@ -501,10 +521,6 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
   tc_fence_after();
   const uint32_t tmem_base = S.tmem_base;
   const int64_t n_tiles = max((int64_t)0, min(run, S.total - begin));
-  Walk<N, kSel> walk;
-  walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
-  Seg s;
-
   if (threadIdx.x == 0) {  // the join's description of the unit this run begins in
     JoinDesc d;
     d.rows = 0;
@@ -512,7 +528,9 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
     d.first = d.last = begin;
     d.q0 = d.hk = d.row0 = 0;
     if (n_tiles > 0) {
-      Walk<N, kSel> w = walk;
+      Walk<N, kSel> w;
+      Seg s;
+      w.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
       w.next(t, s);
       d.rows = s.valid ? s.rows : 0;
       d.first = begin - s.tile0;
@@ -524,202 +542,210 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
     t.desc[blockIdx.x] = d;
   }
 
-  if (warp > kMma) {
-    // ---------------- loaders: positions -> cache rows -> copies ----------------
-    const int lw = warp - kMma - 1, tid = lw * 32 + lane;
-    constexpr int kElt = kFp8 ? 1 : 2, kUnits = D * kElt / 16;  // 16-byte units of a cache row
-    constexpr int kRowsAt = 32 / kUnits;                        // rows a warp copies at a time
-    constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
+  if (warp >= kSoftWarps + 1 + kLookWarps) {
+    // ---------------- copy warps: cache rows -> ring ----------------
+    set_regs<C::kCopyRegs, false>();
+    const int w = warp - (kSoftWarps + 1 + kLookWarps), kv = w >> 3, row0 = (w & 7) * 16;
+    constexpr int kElt = kFp8 ? 1 : 2, kUnits = D * kElt / 16;   // 16-byte units of a cache row
+    constexpr int kRowsAt = 32 / kUnits, kTimes = 16 / kRowsAt;  // rows a warp copies at a time, of its 16
     const int unit = lane % kUnits, sub = lane / kUnits;
     const bool unit_ok = unit * 16 < a.d * kElt;
-    const int64_t row_bytes = (int64_t)a.d * kElt;
-    const uint8_t* pages[2] = {static_cast<const uint8_t*>(a.K) + unit * 16, static_cast<const uint8_t*>(a.V) + unit * 16};
-    const float c2 = a.scale * 1.44269504f;
-    int fill = 0, qn = 0, ready = 0;  // tiles asked for, queries, e4m3 tiles converted
+    const uint32_t row_bytes = (uint32_t)(a.d * kElt);
+    const uint8_t* pages = static_cast<const uint8_t*>(kv ? a.V : a.K) + unit * 16;
     bool ok = true;
-
-    // The lookup of a tile's tokens runs over two tiles, so that no load is
-    // waited for: list entries two tiles ahead, page ids one.
-    Walk<N, kSel> wa = walk;
-    Seg sa;
-    sa.tiles = 0;
-    int ja = 0;
-    int a_pos = -1, a_lim = 0, a_b = 0, a_hk = 0;   // entry of the tile after next
-    int b_id = -1, b_off = 0, b_hk = 0;             // page of the next tile's token
-    bool b_seen = false;
-    auto look_entry = [&]() {
-      a_pos = -1;
-      while (ja == sa.tiles) {
-        if (!wa.next(t, sa)) return;
-        ja = 0;
-        if (!sa.valid) sa.tiles = 0;
-      }
-      const int e = (sa.tile0 + ja) * kTile + tid;
-      ++ja;
-      if (e < sa.end) a_pos = kSel ? a.idx[(int64_t)sa.q0 * a.k + e] : e;
-      a_lim = kSel ? sa.lim0 : 0x7fffffff;
-      a_b = sa.b;
-      a_hk = sa.hk;
-    };
-    auto look_page = [&]() {
-      b_seen = a_pos >= 0 && a_pos <= a_lim;
-      b_hk = a_hk;
-      if (b_seen) {
-        const int col = (int)((unsigned)a_pos / (unsigned)a.page);
-        b_off = a_pos - col * a.page;
-        b_id = a.table[(int64_t)a_b * a.max_pages + col];
-      }
-    };
-    // mask and scales of a tile's tokens, for the softmax warps
-    int tok = 0;
-    uint32_t tok_seen = 0;
-    float tok_ks = 0.f, tok_vs = 0.f;
-    auto post_tokens = [&]() {
-      if constexpr (kFp8) {
-        S.ksc[tok % kTok][tid] = tok_ks * c2;
-        S.vsc[tok % kTok][tid] = tok_vs;
-      }
-      if (lane == 0) S.seen[tok % kTok][lw] = tok_seen;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.tok_full[tok % kTok]);
-      ++tok;
-    };
-    auto convert = [&]() {  // e4m3 tile `ready`: this thread's bytes, staged -> ring
-      const int r = ready % C::kSlots;
-      ok = ok && mbar_wait<true>(&S.empty[r], ((ready / C::kSlots) & 1) ^ 1, abort_flag, a.status, 76, budget);
+    auto wait_rows = [&](int n) {  // the rows of tile n are there
+      ok = ok && mbar_wait<true>(&S.tok_full[n % kTok], (n / kTok) & 1, abort_flag, a.status, 72, budget);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      const uint8_t* src = S.raw[ready % kRaw] + tid * 16;
+    };
+    auto slot_free = [&](int n) {  // the ring slot of tile n's K or V, once it is free
+      const int fill = 2 * n + kv, r = fill % C::kSlots;
+      ok = ok && mbar_wait<true>(&S.empty[r], ((fill / C::kSlots) & 1) ^ 1, abort_flag, a.status, 71, budget);
+      ok = __all_sync(0xffffffffu, ok);
+      return r;
+    };
+    if constexpr (!kFp8) {
+      for (int n = 0;; ++n) {
+        wait_rows(n);
+        if (!ok || S.rows[n % kTok][0] == kEnd) break;
+        const int r = slot_free(n);
+        if (!ok) break;
+        const int* rows = S.rows[n % kTok] + row0 + sub;
+        const uint32_t dst = smem_u32(S.ring[r]) + (unit >> 3) * kTile * 128 + (row0 + sub) * 128;
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const int row = rows[i * kRowsAt];
+          const bool in = row >= 0 && unit_ok;
+          copy16(dst + i * kRowsAt * 128 + (((unit & 7) ^ ((i * kRowsAt + sub) & 7)) << 4),
+                 in ? pages + (uint64_t)(uint32_t)row * row_bytes : static_cast<const uint8_t*>(a.K), in);
+        }
+        copies_arrive(&S.full[r]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tok_empty[n % kTok]);
+      }
+      // never leave with a copy in flight
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      uint4 raw[kTimes];  // a tile's bytes
+      auto load_unit = [&](int i, int row) {
+        uint4& v = raw[i];
+        v = make_uint4(0, 0, 0, 0);
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+            "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+            : "l"(pages + (uint64_t)(uint32_t)row * row_bytes), "r"((uint32_t)(row >= 0 && unit_ok)));
+      };
       // the second 64-element chunk's lanes write their odd unit first, so that no two lanes of a row share banks
       const int flip = (unit >> 2) & 1;
-      uint8_t* dst0 = S.ring[r] + (unit >> 2) * kTile * 128;
+      wait_rows(0);
+      bool more = ok && S.rows[0][0] != kEnd;
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(src + i * kLoadWarps * 512);
-        const uint2 w0 = e4m3x4_to_bf16(raw.x), w1 = e4m3x4_to_bf16(raw.y), w2 = e4m3x4_to_bf16(raw.z),
-                    w3 = e4m3x4_to_bf16(raw.w);
-        const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-        const int row = lw * 32 + i * kRowsAt + sub, u0 = (unit & 3) * 2, sw = row & 7;
-        uint8_t* dst = dst0 + row * 128;
-        *reinterpret_cast<uint4*>(dst + (((u0 + flip) ^ sw) << 4)) = flip ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + (((u0 + (flip ^ 1)) ^ sw) << 4)) = flip ? lo : hi;
+      for (int i = 0; i < kTimes; ++i) load_unit(i, more ? S.rows[0][row0 + sub + i * kRowsAt] : -1);
+      for (int n = 0; ok && more; ++n) {
+        wait_rows(n + 1);
+        const int r = slot_free(n);
+        if (!ok) break;
+        const int* rows = S.rows[(n + 1) % kTok] + row0 + sub;
+        more = S.rows[(n + 1) % kTok][0] != kEnd;
+        uint8_t* dst0 = S.ring[r] + (unit >> 2) * kTile * 128;
+#pragma unroll
+        for (int i = 0; i < kTimes; ++i) {
+          const uint2 w0 = e4m3x4_to_bf16(raw[i].x), w1 = e4m3x4_to_bf16(raw[i].y), w2 = e4m3x4_to_bf16(raw[i].z),
+                      w3 = e4m3x4_to_bf16(raw[i].w);
+          load_unit(i, more ? rows[i * kRowsAt] : -1);  // behind the last tile the entry holds no rows
+          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+          const int at = row0 + i * kRowsAt + sub, u0 = (unit & 3) * 2, sw = at & 7;
+          uint8_t* dst = dst0 + at * 128;
+          *reinterpret_cast<uint4*>(dst + (((u0 + flip) ^ sw) << 4)) = flip ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + (((u0 + (flip ^ 1)) ^ sw) << 4)) = flip ? lo : hi;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.full[r]);
+          mbar_arrive(&S.tok_empty[n % kTok]);
+        }
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.full[r]);
-      ++ready;
+    }
+  } else if (warp > kMma) {
+    // ---------------- lookup warps: positions -> cache rows, masks, scales; queries ----------------
+    set_regs<C::kMidRegs, false>();
+    const int lw = warp - kMma - 1;
+    Walk<N, kSel> walk;
+    walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+    Seg s;
+    int n = 0, qn = 0;  // tiles, segments
+    bool ok = true;
+    auto tile_free = [&]() {
+      ok = ok && mbar_wait<true>(&S.tok_empty[n % kTok], ((n / kTok) & 1) ^ 1, abort_flag, a.status, 73, budget);
+      ok = __all_sync(0xffffffffu, ok);
     };
-
-    look_entry();
-    look_page();
-    look_entry();
     while (ok && walk.next(t, s)) {
       if (!s.valid) continue;
-      {  // the segment's queries
-        const int qb = qn % C::kQBufs;
-        if (kFp8 && C::kQBufs == 1) {
-          // the only query buffer is free once the last keys, still staged, are multiplied
-          if (tok * 2 < fill) post_tokens();
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          while (ok && ready < fill) convert();
-        }
-        if (ok && qn >= C::kQBufs)
-          ok = mbar_wait<true>(&S.q_empty[qb], (qn / C::kQBufs - 1) & 1, abort_flag, a.status, 70, budget);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint8_t* Q = static_cast<const uint8_t*>(a.Q);
-        constexpr int kQUnits = D / 8;
-#pragma unroll 4
-        for (int e = tid; e < N * kQUnits; e += kLoadWarps * 32) {
-          const int r = e / kQUnits, u = e % kQUnits, rr = s.row0 + r, j = rr / g;
-          const bool in = r < s.rows && u * 8 < a.d;
-          const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
-          uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-          if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (in) v = *reinterpret_cast<const uint4*>(Q + at * 2);
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                           __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
-          } else {
-            copy16(smem_u32(dst), Q + at * 2, in);
-          }
-        }
-        if constexpr (kFp8) {
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.q_full[qb]);
+      // the segment's queries, a third each
+      const int qb = qn % C::kQBufs;
+      if (qn >= C::kQBufs)
+        ok = mbar_wait<true>(&S.q_empty[qb], (qn / C::kQBufs - 1) & 1, abort_flag, a.status, 70, budget);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint8_t* Q = static_cast<const uint8_t*>(a.Q);
+      constexpr int kQUnits = D / 8;
+#pragma unroll 2
+      for (int e = lw * 32 + lane; e < N * kQUnits; e += kLookWarps * 32) {
+        const int r = e / kQUnits, u = e % kQUnits, rr = s.row0 + r, j = rr / g;
+        const bool in = r < s.rows && u * 8 < a.d;
+        const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
+        uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+        if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (in) v = *reinterpret_cast<const uint4*>(Q + at * 2);
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                         __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
         } else {
-          copies_arrive(&S.q_full[qb]);
+          copy16(smem_u32(dst), Q + at * 2, in);
         }
-        ++qn;
       }
-      for (int j = 0; ok && j < s.tiles; ++j) {
-        if constexpr (kFp8)
-          if (tok * 2 < fill) post_tokens();  // the tile before: its scales have come
-        int row = -1;
-        if (b_seen) {
-          if ((unsigned)b_id < (unsigned)a.n_pages)
-            row = b_id * t.row_stride_page + b_off * a.Hkv + b_hk;
-          else
-            report_error(a.status, DSA_ERR_INVALID_ARG, 41);
-        }
-        if constexpr (kSel) tok_seen = __ballot_sync(0xffffffffu, b_seen);
-        if constexpr (kFp8) {
-          tok_ks = tok_vs = 0.f;
-          if (row >= 0) {
-            const int64_t at = ((int64_t)b_id * a.page + b_off) * a.Hkv + b_hk;
-            tok_ks = a.K_scale[at];
-            tok_vs = a.V_scale[at];
-          }
-        } else if constexpr (kSel) {
-          post_tokens();
-        }
-        look_page();
-        look_entry();
+      if constexpr (kFp8) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.q_full[qb]);
+      } else {
+        copies_arrive(&S.q_full[qb]);
+      }
+      ++qn;
+      for (int j = 0; j < s.tiles; ++j, ++n) {
+        if (n % kLookWarps != lw) continue;  // the tiles in turn
+        const int tk = n % kTok, e0 = (s.tile0 + j) * kTile + lane;
+        int pos[4], id[4], off[4], row[4];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++fill) {
-          uint32_t dst;
-          if constexpr (kFp8) {  // this thread has read what the stage held
-            dst = smem_u32(S.raw[fill % kRaw]) + tid * 16;
-          } else {
-            const int r = fill % C::kSlots;
-            ok = ok && mbar_wait<true>(&S.empty[r], ((fill / C::kSlots) & 1) ^ 1, abort_flag, a.status, 71, budget);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            dst = smem_u32(S.ring[r]) + (unit >> 3) * kTile * 128 + (lw * 32 + sub) * 128;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int e = e0 + i * 32;
+          pos[i] = -1;
+          if (e < s.end) pos[i] = kSel ? a.idx[(int64_t)s.q0 * a.k + e] : e;
+        }
 #pragma unroll
-          for (int i = 0; i < kUnits; ++i) {
-            const int src = __shfl_sync(0xffffffffu, row, i * kRowsAt + sub);
-            const bool in = src >= 0 && unit_ok;
-            const uint8_t* from = pages[kv] + (in ? src * row_bytes : -(int64_t)unit * 16);
-            if constexpr (kFp8)
-              copy16(dst + i * kLoadWarps * 512, from, in);
-            else
-              copy16(dst + i * kRowsAt * 128 + (((unit & 7) ^ ((i * kRowsAt + sub) & 7)) << 4), from, in);
+        for (int i = 0; i < 4; ++i) {
+          if (kSel && pos[i] > s.lim0) pos[i] = -1;
+          id[i] = -1;
+          off[i] = 0;
+          if (pos[i] >= 0) {
+            const int col = (int)((unsigned)pos[i] / (unsigned)a.page);
+            off[i] = pos[i] - col * a.page;
+            id[i] = a.table[(int64_t)s.b * a.max_pages + col];
           }
-          if constexpr (kFp8) {
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (fill - ready >= kRaw - 1) {
-              asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-              convert();
-              if (!ok) break;
+        }
+        float ks[4], vs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          row[i] = -1;
+          ks[i] = vs[i] = 0.f;
+          if ((unsigned)id[i] < (unsigned)a.n_pages) {
+            row[i] = id[i] * t.row_stride_page + off[i] * a.Hkv + s.hk;
+            if constexpr (kFp8) {
+              const int64_t at = ((int64_t)id[i] * a.page + off[i]) * a.Hkv + s.hk;
+              ks[i] = a.K_scale[at];
+              vs[i] = a.V_scale[at];
             }
-          } else {
-            copies_arrive(&S.full[fill % C::kSlots]);
+          } else if (pos[i] >= 0) {
+            report_error(a.status, DSA_ERR_INVALID_ARG, 41);
           }
         }
+        tile_free();
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          S.rows[tk][i * 32 + lane] = row[i];
+          if constexpr (kFp8) {
+            S.ksc[tk][i * 32 + lane] = ks[i] * (a.scale * 1.44269504f);
+            S.vsc[tk][i * 32 + lane] = vs[i];
+          }
+          if constexpr (kSel) {
+            const uint32_t seen = __ballot_sync(0xffffffffu, pos[i] >= 0);
+            if (lane == 0) S.seen[tk][i] = seen;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.tok_full[tk]);
       }
     }
-    // never leave with a copy in flight
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if constexpr (kFp8) {
-      if (ok && tok * 2 < fill) post_tokens();
-      while (ok && ready < fill) convert();
+    if (n % kLookWarps == lw) {  // the end, for the copy warps
+      tile_free();
+      if (ok) {
+        if (lane == 0) {
+          S.rows[n % kTok][0] = kEnd;
+          mbar_arrive(&S.tok_full[n % kTok]);
+        }
+        __syncwarp();
+      }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kMma) {
     // ---------------- MMA issuer: the warp waits, one lane issues ----------------
+    set_regs<C::kMidRegs, false>();
+    Walk<N, kSel> walk;
+    walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+    Seg s;
     constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
     constexpr uint32_t kIdescO = C::kRows ? idesc_bf16_f32(128, D) | (1u << 16)                // V along N
                                           : idesc_bf16_f32(D, N) | (1u << 15) | (1u << 16);  // V^T along M, P along N
@@ -817,6 +843,10 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
     __syncwarp();
   } else {
     // ---------------- softmax ----------------
+    set_regs<C::kSoftRegs, true>();
+    Walk<N, kSel> walk;
+    walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+    Seg s;
     const int wg = warp >> 2, wq = warp & 3, tid = threadIdx.x & 127;
     constexpr int kGroup = C::kRows ? 256 : 128;
     const int bar = C::kRows ? 1 : 1 + wg;
@@ -992,7 +1022,10 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&S.p_full[n & 1]);
+          if (lane == 0) {
+            mbar_arrive(&S.p_full[n & 1]);
+            if constexpr (kSel || kFp8) mbar_arrive(&S.tok_empty[tk]);
+          }
           if (j == 0) store_output();
         }
         // ---- the segment's sums ----
@@ -1183,7 +1216,10 @@ __global__ void __launch_bounds__(Cfg<N, D, kFp8>::kWarps * 32, 1)
           fence_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&S.p_full[n & 1]);
+          if (lane == 0) {
+            mbar_arrive(&S.p_full[n & 1]);
+            if constexpr (kSel || kFp8) mbar_arrive(&S.tok_empty[tk]);
+          }
           if (j == 0) store_output();
         }
         // ---- the segment's sums ----
@@ -1349,7 +1385,7 @@ static int launch_attend_tc(const TcAttend& t, int grid, cudaStream_t st) {
       return DSA_ERR_CUDA;
     configured.fetch_or(bit, std::memory_order_release);
   }
-  attend_tc_kernel<N, D, kFp8, kSel><<<grid, C::kWarps * 32, kSmem, st>>>(t);
+  attend_tc_kernel<N, D, kFp8, kSel><<<grid, kWarps * 32, kSmem, st>>>(t);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (grid == 1 || (kSel && t.run % t.unit_tiles == 0)) return DSA_OK;  // no unit is divided
   // The join may take its place on the SMs while the last tiles run; it waits
