@@ -44,90 +44,106 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _need(t: torch.Tensor, what: str, dtype, shape, device=None):
-    """`t` is a contiguous CUDA tensor of this dtype and shape (None: any size there)."""
+def _refuse(t: torch.Tensor, what: str, dtype, shape, device):
+    """Says what is wrong with a tensor that `_need` does not take."""
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on a CUDA device (the cache has no CPU path)")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not {device}")
+    raise ValueError(f"{what} is on {t.device}, not {device}")
 
 
-def _pool(K, V, K_scale, V_scale, device, Hkv=None, d=None) -> Tuple[int, int]:
+def _need(t: torch.Tensor, what: str, dtype, shape, device):
+    """`t` is a contiguous tensor of this dtype and shape on this CUDA device."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous() and t.device == device):
+        _refuse(t, what, dtype, shape, device)
+
+
+def _pool(K, V, K_scale, V_scale, device, Hkv, d) -> Tuple[int, int]:
     """Checks the pages of a cache (V may be absent); (element type, page stride in elements)."""
     code = _type(K, "K_pages", True)
-    if K.dim() != 4 or (Hkv is not None and tuple(K.shape[2:]) != (Hkv, d)):
-        raise ValueError("K_pages must be [n_pages, page, Hkv, d]" + (f" with Hkv, d = {Hkv}, {d}" if Hkv else ""))
-    n, page, hk, dd = K.shape
-    stride = K.stride(0) if n > 1 else page * hk * dd
+    shape = K.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != d:
+        raise ValueError(f"K_pages must be [n_pages, page, Hkv, d] with Hkv, d = {Hkv}, {d}")
+    n, page = shape[0], shape[1]
+    inner = page * Hkv * d
+    stride = K.stride(0) if n > 1 else inner
     for t, what in ((K, "K_pages"), (V, "V_pages")):
         if t is None:
             continue
         if not t.is_cuda or t.device != device:
             raise ValueError(f"{what} must be on {device}")
-        if t.shape != K.shape or t.dtype != K.dtype:
+        if t.shape != shape or t.dtype is not K.dtype:
             raise ValueError(f"{what} must have K_pages' shape and dtype")
-        if not t[0].is_contiguous() or (n > 1 and t.stride(0) != stride) or stride < page * hk * dd:
+        if t.is_contiguous() and (n <= 1 or stride == inner):
+            continue
+        if not t[0].is_contiguous() or (n > 1 and t.stride(0) != stride) or stride < inner:
             raise ValueError(f"{what}: the dimensions [page, Hkv, d] must be contiguous, K and V pages equally far apart")
-    if (code == DSA_DTYPE_FP8_E4M3) != (K_scale is not None) or \
-            (code == DSA_DTYPE_FP8_E4M3 and V is not None) != (V_scale is not None):
+    fp8 = code == DSA_DTYPE_FP8_E4M3
+    if fp8 != (K_scale is not None) or (fp8 and V is not None) != (V_scale is not None):
         raise ValueError("e4m3 pages (and only they) come with K_scale and V_scale")
-    for t, what in ((K_scale, "K_scale"), (V_scale, "V_scale")):
-        if t is not None:
-            _need(t, what, torch.float32, (n, page, hk), device)
+    if K_scale is not None:
+        _need(K_scale, "K_scale", torch.float32, (n, page, Hkv), device)
+    if V_scale is not None:
+        _need(V_scale, "V_scale", torch.float32, (n, page, Hkv), device)
     return code, stride
 
 
-@contextlib.contextmanager
+_same = contextlib.nullcontext()
+
+
 def _on(device: torch.device, stream):
-    """Makes the tensors' device current and yields the stream's handle; what is allocated inside belongs to it."""
-    if stream is None:
-        if torch.cuda.current_device() == device.index:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.device(device):
-                yield torch.cuda.current_stream().cuda_stream
-    else:
+    """(a context that makes the tensors' device and the call's stream current, or None when they are; the stream's
+    handle): what is allocated inside belongs to that stream."""
+    if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+        return torch.cuda.stream(stream), stream.cuda_stream
+    index = device.index
+    if torch.cuda.current_device() == index:
+        return None, _raw_stream(index)
+    return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of a device's current stream (torch's accessor for compiled code: 0.1 us, the public one takes 3)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _workspace(nbytes: int, device, workspace):
-    if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        if workspace.numel() * workspace.element_size() < nbytes:
-            raise ValueError(f"workspace has {workspace.numel() * workspace.element_size()} bytes, needs {nbytes}")
-        return workspace
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if workspace is None:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device), nbytes
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    size = workspace.numel() * workspace.element_size()
+    if size < nbytes:
+        raise ValueError(f"workspace has {size} bytes, needs {nbytes}")
+    return workspace, size
 
 
 @functools.lru_cache(maxsize=1024)
 def _bytes(name: str, device, *args) -> int:
     n = _sz(0)
     with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
-        _check(getattr(lib(), name)(*args, ctypes.byref(n)), name)
+        _check(getattr(lib(), name + "_workspace_size")(*args, ctypes.byref(n)), name)
     return int(n.value)
 
 
 def page_plan_workspace_bytes(B, max_tokens) -> int:
-    return _bytes("dsa_page_plan_workspace_size", None, B, max_tokens)
+    return _bytes("dsa_page_plan", None, B, max_tokens)
 
 
 def attend_paged_workspace_bytes(B, total_q, max_q, Hq, Hkv, d, q_dtype, kv_dtype) -> int:
-    return _bytes("dsa_attend_paged_workspace_size", torch.cuda.current_device(), B, total_q, max_q, Hq, Hkv, d,
+    return _bytes("dsa_attend_paged", torch.cuda.current_device(), B, total_q, max_q, Hq, Hkv, d,
                   q_dtype, kv_dtype)
 
 
 def attend_selected_workspace_bytes(B, total_q, k, Hq, Hkv, d, q_dtype, kv_dtype) -> int:
-    return _bytes("dsa_attend_selected_workspace_size", torch.cuda.current_device(), B, total_q, k, Hq, Hkv, d,
+    return _bytes("dsa_attend_selected", torch.cuda.current_device(), B, total_q, k, Hq, Hkv, d,
                   q_dtype, kv_dtype)
 
 
@@ -147,34 +163,40 @@ def dsa_page_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     the table stays, the step has no tokens, and the status word tells.
     """
     dev = lens.device
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    _need(lens, "lens", torch.int32, (B,))
-    _need(new_lens, "new_lens", torch.int32, (B,), dev)
-    _need(block_table, "block_table", torch.int32, (B, None), dev)
-    _need(free_pages, "free_pages", torch.int32, (None,), dev)
-    _need(used, "used", torch.int32, (1,), dev)
-    max_tokens = int(max_tokens)
+    if lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("lens must be [B], block_table [B, max_pages], free_pages [n_free]")
+    B, i32 = lens.shape[0], torch.int32
+    width, n_free, max_tokens = block_table.shape[1], free_pages.shape[0], int(max_tokens)
+    _need(lens, "lens", i32, (B,), dev)
+    _need(new_lens, "new_lens", i32, (B,), dev)
+    _need(block_table, "block_table", i32, (B, width), dev)
+    _need(free_pages, "free_pages", i32, (n_free,), dev)
+    _need(used, "used", i32, (1,), dev)
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    with _on(dev, stream) as st:
+    context, st = _on(dev, stream)
+    with context or _same:
+        i64, empty = torch.int64, torch.empty
         if out is None:
-            i32 = functools.partial(torch.empty, dtype=torch.int32, device=dev)
-            out = (i32(B + 1), torch.empty(max_tokens, dtype=torch.int64, device=dev), i32(max_tokens), i32(B), i32(1))
+            out = (empty(B + 1, dtype=i32, device=dev), empty(max_tokens, dtype=i64, device=dev),
+                   empty(max_tokens, dtype=i32, device=dev), empty(B, dtype=i32, device=dev),
+                   empty(1, dtype=i32, device=dev))
             if B == 0:  # nothing is launched: the answer of a step without requests
                 out[0].zero_(), out[1].fill_(-1), out[2].fill_(-1), out[4].copy_(used)
         else:
             for t, what, dtype, n in zip(out, ("q_offsets", "slots", "positions", "lens_out", "used_out"),
-                                         (torch.int32, torch.int64, torch.int32, torch.int32, torch.int32),
-                                         (B + 1, max_tokens, max_tokens, B, 1)):
+                                         (i32, i64, i32, i32, i32), (B + 1, max_tokens, max_tokens, B, 1)):
                 _need(t, what, dtype, (n,), dev)
-        ws = _workspace(page_plan_workspace_bytes(B, max_tokens), dev, workspace)
+        ws, size = _workspace(page_plan_workspace_bytes(B, max_tokens), dev, workspace)
         q_offsets, slots, positions, lens_out, used_out = out
-        _check(lib().dsa_page_plan(_p(lens), _p(new_lens), _p(free_pages), free_pages.numel(), _p(used), B, int(page),
-                                   int(n_pages), block_table.shape[1], max_tokens, _p(block_table), _p(q_offsets),
-                                   _p(slots), _p(positions), _p(lens_out), _p(used_out), _p(ws),
-                                   ws.numel() * ws.element_size(), st), "dsa_page_plan")
+        r = lib().dsa_page_plan(lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), n_free, used.data_ptr(), B,
+                                int(page), int(n_pages), width, max_tokens, block_table.data_ptr(), q_offsets.data_ptr(),
+                                slots.data_ptr(), positions.data_ptr(), lens_out.data_ptr(), used_out.data_ptr(),
+                                ws.data_ptr(), size, st)
+        if r:
+            _check(r, "dsa_page_plan")
         if check:
-            _check(lib().dsa_check_status(_p(ws), st), "device status")
+            _check(lib().dsa_check_status(ws.data_ptr(), st), "device status")
     return out
 
 
@@ -190,61 +212,74 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
     """
     if k.dim() != 3:
         raise ValueError("k must be [T, Hkv, d]")
-    dev, (T, Hkv, d) = k.device, k.shape
+    dev, shape = k.device, k.shape
+    T, Hkv, d = shape
     sd = _type(k, "k", False)
-    _need(k, "k", k.dtype, (T, Hkv, d))
+    _need(k, "k", k.dtype, shape, dev)
     if (v is None) != (V_pages is None):
         raise ValueError("v and V_pages come together")
     if v is not None:
-        _need(v, "v", k.dtype, (T, Hkv, d), dev)
+        _need(v, "v", k.dtype, shape, dev)
     _need(slots, "slots", torch.int64, (T,), dev)
     kd, stride = _pool(K_pages, V_pages, K_scale, V_scale, dev, Hkv, d)
-    with _on(dev, stream) as st:
-        ws = _workspace(256, dev, workspace)
-        _check(lib().dsa_page_append(_p(k), _p(v), _p(slots), T, Hkv, d, sd, kd, _p(K_pages), _p(V_pages),
-                                     _p(K_scale), _p(V_scale), K_pages.shape[0], K_pages.shape[1], stride, _p(ws),
-                                     ws.numel() * ws.element_size(), st), "dsa_page_append")
+    n_pages, page = K_pages.shape[:2]
+    context, st = _on(dev, stream)
+    with context or _same:
+        ws, size = _workspace(256, dev, workspace)
+        r = lib().dsa_page_append(k.data_ptr(), _p(v), slots.data_ptr(), T, Hkv, d, sd, kd, K_pages.data_ptr(),
+                                  _p(V_pages), _p(K_scale), _p(V_scale), n_pages, page, stride, ws.data_ptr(), size, st)
+        if r:
+            _check(r, "dsa_page_append")
         if check:
-            _check(lib().dsa_check_status(_p(ws), st), "device status")
+            _check(lib().dsa_check_status(ws.data_ptr(), st), "device status")
 
 
 def _attend(name, Q, K, V, block_table, lens, q_offsets, idx, max_q, scale, K_scale, V_scale, out, lse, workspace,
             stream, check):
-    if Q.dim() != 3 or K.dim() != 4:
-        raise ValueError("Q must be [total_q, Hq, d], K_pages [n_pages, page, Hkv, d]")
-    dev, (rows, Hq, d) = Q.device, Q.shape
+    if Q.dim() != 3 or K.dim() != 4 or lens.dim() != 1 or block_table.dim() != 2 or (idx is not None and idx.dim() != 2):
+        raise ValueError("Q must be [total_q, Hq, d], K_pages [n_pages, page, Hkv, d], lens [B], block_table "
+                         "[B, max_pages], idx [total_q, k]")
+    dev, dtype, shape, i32 = Q.device, Q.dtype, Q.shape, torch.int32
+    rows, Hq, d = shape
     n_pages, page, Hkv, _ = K.shape
     qd = _type(Q, "Q", False)
-    _need(Q, "Q", Q.dtype, (rows, Hq, d))
+    _need(Q, "Q", dtype, shape, dev)
     kd, stride = _pool(K, V, K_scale, V_scale, dev, Hkv, d)
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    _need(lens, "lens", torch.int32, (B,), dev)
-    _need(q_offsets, "q_offsets", torch.int32, (B + 1,), dev)
-    _need(block_table, "block_table", torch.int32, (B, None), dev)
+    B, width = lens.shape[0], block_table.shape[1]
+    _need(lens, "lens", i32, (B,), dev)
+    _need(q_offsets, "q_offsets", i32, (B + 1,), dev)
+    _need(block_table, "block_table", i32, (B, width), dev)
+    k = max_q
     if idx is not None:
-        _need(idx, "idx", torch.int32, (rows, None), dev)
+        k = idx.shape[1]
+        _need(idx, "idx", i32, (rows, k), dev)
     sc = None if scale is None else ctypes.byref(ctypes.c_float(scale))
-    with _on(dev, stream) as st:
+    context, st = _on(dev, stream)
+    with context or _same:
         if out is None:
             out = torch.empty_like(Q)
         else:
-            _need(out, "out", Q.dtype, (rows, Hq, d), dev)
+            _need(out, "out", dtype, shape, dev)
         if lse is True:
             lse = torch.empty((rows, Hq), dtype=torch.float32, device=dev)
         elif lse is not None:
             _need(lse, "lse", torch.float32, (rows, Hq), dev)
-        mid = max_q if idx is None else idx.shape[1]
-        ws = _workspace(_bytes(name + "_workspace_size", dev.index, B, rows, mid, Hq, Hkv, d, qd, kd), dev, workspace)
-        head = (_p(Q), _p(K), _p(V), _p(K_scale), _p(V_scale), _p(block_table), _p(lens), _p(q_offsets))
-        tail = (n_pages, page, stride, block_table.shape[1], Hq, Hkv, d, sc, qd, kd, _p(out), _p(lse), _p(ws),
-                ws.numel() * ws.element_size(), st)
+        ws, size = _workspace(_bytes(name, dev.index, B, rows, k, Hq, Hkv, d, qd, kd), dev, workspace)
+        L = lib()
         if idx is None:
-            r = lib().dsa_attend_paged(*head, B, rows, max_q, *tail)
+            r = L.dsa_attend_paged(Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(K_scale), _p(V_scale),
+                                   block_table.data_ptr(), lens.data_ptr(), q_offsets.data_ptr(), B, rows, max_q,
+                                   n_pages, page, stride, width, Hq, Hkv, d, sc, qd, kd, out.data_ptr(), _p(lse),
+                                   ws.data_ptr(), size, st)
         else:
-            r = lib().dsa_attend_selected(*head, _p(idx), idx.shape[1], B, rows, *tail)
-        _check(r, name)
+            r = L.dsa_attend_selected(Q.data_ptr(), K.data_ptr(), V.data_ptr(), _p(K_scale), _p(V_scale),
+                                      block_table.data_ptr(), lens.data_ptr(), q_offsets.data_ptr(), idx.data_ptr(), k,
+                                      B, rows, n_pages, page, stride, width, Hq, Hkv, d, sc, qd, kd, out.data_ptr(),
+                                      _p(lse), ws.data_ptr(), size, st)
+        if r:
+            _check(r, name)
         if check:
-            _check(lib().dsa_check_status(_p(ws), st), "device status")
+            _check(L.dsa_check_status(ws.data_ptr(), st), "device status")
     return out if lse is None else (out, lse)
 
 

@@ -5,13 +5,17 @@
 // ceil((len + new) / P).  Two exclusive sums over the requests (new tokens,
 // new pages) give q_offsets and each request's first entry of the free list;
 // after that every table entry and every token is independent of the others:
-// a token finds its request by bisection in q_offsets.  The sums run in one
-// block, so their order is fixed and no atomics are needed.
+// a token finds its request by bisection in q_offsets.  The sums run inside a
+// block, so their order is fixed and no atomics are needed.  A decode step is
+// all latency: up to 2048 requests, every block forms the sums for itself in
+// shared memory and fills its share, one launch in all.  With more, or when
+// lens or used is updated in place (a block may read it after another has
+// written it), one block forms the sums and a second launch fills.
 //
 // Cache write.  A row is Hkv * d contiguous elements at its slot: a copy, or
-// for e4m3 pages one pass per (row, head) that holds the d elements in
-// registers, reduces their amax across the lanes, and stores the bytes and
-// the scale.
+// for e4m3 pages the smallest power of two of lanes that holds a head's d
+// elements, eight a lane: amax by shuffles, eight bytes stored at once.  The
+// bound is memory: each row is read and written once.
 #include "dsa_paged.cuh"
 
 namespace dsa {
@@ -78,13 +82,22 @@ __device__ __forceinline__ bool plan_request(const PlanArgs& a, int b, int64_t (
   return true;
 }
 
+// The checks over both sums' totals, by every thread of a block; ok: this
+// thread's requests are valid.
+__device__ __forceinline__ bool plan_fits(const PlanArgs& a, bool ok, int used, const int64_t (&total)[2], bool report) {
+  ok = __syncthreads_and(ok && used >= 0 && used <= a.n_free && total[0] <= a.max_tokens);
+  const bool enough = total[1] <= (int64_t)a.n_free - used;
+  if (report && threadIdx.x == 0 && !(ok && enough)) report_error(a.status, ok ? DSA_ERR_PAGES : DSA_ERR_INVALID_ARG, 50);
+  return ok && enough;
+}
+
 // Both sums and the checks, by one block.  Leaves q_off, first, lens_out,
 // used_out and the entry state; a step that fails leaves zero sums.
 __device__ __forceinline__ void plan_sums(const PlanArgs& a) {
   __shared__ int64_t warp_sum[kPlanThreads / 32][2];
   const int used = a.used[0];
   int64_t total[2] = {0, 0};
-  bool ok = used >= 0 && used <= a.n_free;
+  bool ok = true;
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {  // totals first: all or nothing
     const int b = b0 + threadIdx.x;
     int64_t v[2] = {0, 0}, t[2];
@@ -94,10 +107,7 @@ __device__ __forceinline__ void plan_sums(const PlanArgs& a) {
     total[0] += t[0];
     total[1] += t[1];
   }
-  ok = __syncthreads_and(ok && total[0] <= a.max_tokens);
-  const bool enough = total[1] <= (int64_t)a.n_free - used;
-  if (threadIdx.x == 0 && !(ok && enough)) report_error(a.status, ok ? DSA_ERR_PAGES : DSA_ERR_INVALID_ARG, 50);
-  ok = ok && enough;
+  ok = plan_fits(a, ok, used, total, true);
   int64_t base[2] = {0, 0};
   for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
@@ -145,52 +155,140 @@ __device__ __forceinline__ int fresh_page(const PlanArgs& a, int used, int i) {
   return -1;
 }
 
-// Table entries and tokens t, t + step, ...
-__device__ __forceinline__ void plan_fill(const PlanArgs& a, int64_t t, int64_t step) {
-  const int n_new = a.q_off[a.B], n_fresh = a.first[a.B], used = a.state[0];
+// Table entries t, t + step, ... and tokens 4 t .. 4 t + 3, 4 (t + step) ...
+// q_off, first [B + 1] and lens [B] (new tokens included): the sums, in
+// global or shared memory.
+__device__ __forceinline__ void plan_fill(const PlanArgs& a, const int32_t* q_off, const int32_t* first,
+                                          const int32_t* lens, int used, int64_t t, int64_t step) {
+  const int n_new = q_off[a.B], n_fresh = first[a.B];
   for (int64_t i = t; i < n_fresh; i += step) {
-    const int b = bisect(a.first, a.B, (int)i);
-    const int m = a.q_off[b + 1] - a.q_off[b], len = a.lens_out[b] - m;
+    const int b = bisect(first, a.B, (int)i);
+    const int len = lens[b] - (q_off[b + 1] - q_off[b]);
     const int held = (int)((len + a.page - 1ll) / a.page);
-    a.table[(int64_t)b * a.max_pages + held + ((int)i - a.first[b])] = fresh_page(a, used, (int)i);
+    a.table[(int64_t)b * a.max_pages + held + ((int)i - first[b])] = fresh_page(a, used, (int)i);
   }
-  for (int64_t i = t; i < a.max_tokens; i += step) {
-    int64_t slot = -1;
-    int pos = -1;
-    if (i < n_new) {
-      const int b = bisect(a.q_off, a.B, (int)i);
-      const int q0 = a.q_off[b], m = a.q_off[b + 1] - q0, len = a.lens_out[b] - m;
-      pos = len + (int)i - q0;
-      const int held = (int)((len + a.page - 1ll) / a.page), col = pos / a.page;
-      int id;
-      if (col < held) {  // the last page the request held already
-        id = a.table[(int64_t)b * a.max_pages + col];
-        if ((unsigned)id >= (unsigned)a.n_pages) {
-          report_error(a.status, DSA_ERR_INVALID_ARG, 52);
-          id = -1;
+  for (int64_t i0 = t * 4; i0 < a.max_tokens; i0 += step * 4) {
+    int64_t slot[4];
+    int pos[4];
+    int b = -1, next = 0, len = 0, held = 0, q0 = 0, col = -1, id = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t i = i0 + e;
+      slot[e] = -1;
+      pos[e] = -1;
+      if (i >= n_new) continue;
+      if (b < 0 || i >= next) {  // another request
+        if (b < 0) {
+          b = bisect(q_off, a.B, (int)i);
+        } else {
+          do ++b;
+          while (q_off[b + 1] <= i);
         }
-      } else {
-        id = fresh_page(a, used, a.first[b] + col - held);
+        q0 = q_off[b];
+        next = q_off[b + 1];
+        len = lens[b] - (next - q0);
+        held = (int)((len + a.page - 1ll) / a.page);
+        col = -1;
       }
-      if (id >= 0) slot = (int64_t)id * a.page + (pos - col * a.page);
+      pos[e] = len + (int)i - q0;
+      const int c = pos[e] / a.page;
+      if (c != col) {  // another page
+        col = c;
+        if (col < held) {  // the last page the request held already
+          id = a.table[(int64_t)b * a.max_pages + col];
+          if ((unsigned)id >= (unsigned)a.n_pages) {
+            report_error(a.status, DSA_ERR_INVALID_ARG, 52);
+            id = -1;
+          }
+        } else {
+          id = fresh_page(a, used, first[b] + col - held);
+        }
+      }
+      if (id >= 0) slot[e] = (int64_t)id * a.page + (pos[e] - col * a.page);
     }
-    a.slots[i] = slot;
-    a.positions[i] = pos;
+    if (i0 + 4 <= a.max_tokens) {  // both arrays start on 16 bytes
+      reinterpret_cast<longlong2*>(a.slots + i0)[0] = make_longlong2(slot[0], slot[1]);
+      reinterpret_cast<longlong2*>(a.slots + i0)[1] = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+      for (int e = 0; i0 + e < a.max_tokens; ++e) {
+        a.slots[i0 + e] = slot[e];
+        a.positions[i0 + e] = pos[e];
+      }
+    }
   }
+}
+
+constexpr int kOneRequests = 2048, kOneThreads = 512;
+
+// The whole plan in one launch: every block forms the sums of all requests.
+__global__ void __launch_bounds__(kOneThreads) page_plan_kernel(const PlanArgs a) {
+  constexpr int kEach = kOneRequests / kOneThreads;
+  __shared__ int32_t q_off[kOneRequests + 1], first[kOneRequests + 1], lens[kOneRequests];
+  __shared__ int64_t warp_sum[kOneThreads / 32][2];
+  const int used = a.used[0], each = (a.B + kOneThreads - 1) / kOneThreads, b0 = threadIdx.x * each;
+  int64_t sum[2] = {0, 0}, total[2], v[kEach][2];
+  int len[kEach];
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    v[i][0] = v[i][1] = 0;
+    len[i] = 0;
+    if (i < each && b0 + i < a.B) ok = plan_request(a, b0 + i, v[i], len[i]) && ok;
+    sum[0] += v[i][0];
+    sum[1] += v[i][1];
+  }
+  block_scan2(sum, total, warp_sum);
+  ok = plan_fits(a, ok, used, total, blockIdx.x == 0);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i < each && b0 + i < a.B) {
+      q_off[b0 + i] = ok ? (int)sum[0] : 0;
+      first[b0 + i] = ok ? (int)sum[1] : 0;
+      lens[b0 + i] = len[i] + (ok ? (int)v[i][0] : 0);
+    }
+    sum[0] += v[i][0];
+    sum[1] += v[i][1];
+  }
+  if (threadIdx.x == 0) {
+    q_off[a.B] = ok ? (int)total[0] : 0;
+    first[a.B] = ok ? (int)total[1] : 0;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < a.B; b += kOneThreads) {
+      a.q_off[b] = q_off[b];
+      a.lens_out[b] = lens[b];
+    }
+    if (threadIdx.x == 0) {
+      a.q_off[a.B] = q_off[a.B];
+      a.used_out[0] = used + first[a.B];
+    }
+  }
+  plan_fill(a, q_off, first, lens, used, (int64_t)blockIdx.x * kOneThreads + threadIdx.x,
+            (int64_t)gridDim.x * kOneThreads);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) page_plan_sums_kernel(const PlanArgs a) { plan_sums(a); }
 
 __global__ void __launch_bounds__(256) page_plan_fill_kernel(const PlanArgs a) {
-  plan_fill(a, (int64_t)blockIdx.x * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.x);
+  plan_fill(a, a.q_off, a.first, a.lens_out, a.state[0], (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
+            (int64_t)gridDim.x * blockDim.x);
 }
 
 int launch_page_plan(const PlanArgs& a, int sms, cudaStream_t st) {
   const NvtxRange nvtx("dsa.page_plan");
-  page_plan_sums_kernel<<<1, kPlanThreads, 0, st>>>(a);
-  const int64_t items = (int64_t)a.max_tokens > a.B ? a.max_tokens : a.B;
-  const int64_t blocks = (items + 255) / 256, most = (int64_t)sms * 8;
-  page_plan_fill_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, st>>>(a);
+  // four tokens a thread; a step hands out no more pages than it adds tokens
+  const int64_t items = ((int64_t)a.max_tokens + 3) / 4;
+  if (a.B <= kOneRequests && a.lens_out != a.lens && a.used_out != a.used) {
+    // 4 us for 8 requests; for 1024 with a million tokens 9 us in 2 blocks a multiprocessor
+    const int64_t blocks = (items + kOneThreads - 1) / kOneThreads, most = (int64_t)sms * 2;
+    page_plan_kernel<<<(int)(blocks < 1 ? 1 : (blocks < most ? blocks : most)), kOneThreads, 0, st>>>(a);
+  } else {
+    const int64_t blocks = (items + 255) / 256, most = (int64_t)sms * 8;
+    page_plan_sums_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    page_plan_fill_kernel<<<(int)(blocks < 1 ? 1 : (blocks < most ? blocks : most)), 256, 0, st>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
@@ -214,27 +312,113 @@ __device__ __forceinline__ int64_t slot_row(const AppendArgs& a, int64_t slot) {
     report_error(a.status, DSA_ERR_INVALID_ARG, 60);
     return -1;
   }
-  const int64_t id = slot / a.page;
+  const int64_t id = slot < ((int64_t)1 << 31) ? (unsigned)slot / (unsigned)a.page : slot / a.page;
   return id * a.page_stride + (slot - id * a.page) * a.Hkv * a.d;
 }
 
-// Same type in source and pool: rows of `units` vectors of type V.
+// Same type in source and pool: rows of `units` vectors of type V, a warp
+// copies 128 of them.
 template <typename V>
 __global__ void __launch_bounds__(256) append_copy_kernel(const AppendArgs a, int units, int per_vec) {
-  const int which = blockIdx.y;
-  const V* src = static_cast<const V*>(a.src[which]);
-  V* pool = static_cast<V*>(a.pool[which]);
-  const int64_t n = (int64_t)a.T * units;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t t = i / units;
+  constexpr int kAt = 4;
+  const int which = blockIdx.y, lane = threadIdx.x & 31, parts = (units + 32 * kAt - 1) / (32 * kAt);
+  const int64_t n = (int64_t)a.T * parts, step = (int64_t)gridDim.x * 8;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < n; w += step) {
+    const int64_t t = parts == 1 ? w : w / parts;
+    const int u0 = (int)(w - t * parts) * 32 * kAt + lane;
+    const V* src = static_cast<const V*>(a.src[which]) + t * units;
+    V x[kAt];
+#pragma unroll
+    for (int i = 0; i < kAt; ++i)
+      if (u0 + 32 * i < units) x[i] = src[u0 + 32 * i];
     const int64_t row = slot_row(a, a.slots[t]);
-    if (row >= 0) pool[row / per_vec + (i - t * units)] = src[i];
+    if (row < 0) continue;
+    V* dst = static_cast<V*>(a.pool[which]) + row / per_vec;
+#pragma unroll
+    for (int i = 0; i < kAt; ++i)
+      if (u0 + 32 * i < units) dst[u0 + 32 * i] = x[i];
   }
 }
 
-// e4m3 pages: one warp a (row, head), lane l holds elements l, l + 32, ...
+// x / scale, correctly rounded, by a multiplication with the rounded
+// reciprocal and one correction of the quotient (Markstein 1990): exact while
+// the remainder does not underflow and the divisor's fraction is not all
+// ones; `exact` takes the division instead.
+__device__ __forceinline__ float divide(float x, float scale, float inv, bool exact) {
+  if (exact) return __fdiv_rn(x, scale);
+  const float q = x * inv;
+  return fmaf(fmaf(-q, scale, x), inv, q);
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// e4m3 pages, d a multiple of 8 and rows on 8 bytes: `lanes` (a power of two)
+// a (row, head), eight elements a lane, two rows in flight.  32768 rows of 8
+// heads of 128, bf16: 204 MB.
 template <typename S>
-__global__ void __launch_bounds__(256) append_e4m3_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256) append_e4m3_kernel(const AppendArgs a, int lanes) {
+  constexpr int kAt = 2;
+  const int which = blockIdx.y, lane = threadIdx.x & (lanes - 1);
+  const S* src = static_cast<const S*>(a.src[which]);
+  uint8_t* pool = static_cast<uint8_t*>(a.pool[which]);
+  const int n = a.T * a.Hkv, per_block = 256 / lanes;  // fewer than 2^31 rows (host)
+  const bool mine = lane * 8 < a.d;
+  for (int64_t r0 = (int64_t)blockIdx.x * kAt * per_block; r0 < n; r0 += (int64_t)gridDim.x * kAt * per_block) {
+    float x[kAt][8];
+    int64_t slot[kAt];
+    int h[kAt];
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const int64_t r = r0 + i * per_block + threadIdx.x / lanes;
+      slot[i] = -1;
+      h[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      if (r < n) {
+        const int t = (int)((unsigned)r / (unsigned)a.Hkv);
+        h[i] = (int)r - t * a.Hkv;
+        slot[i] = a.slots[t];
+        if (mine) load8(src + r * a.d + lane * 8, x[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float scale = fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f), inv = __frcp_rn(scale);
+      const bool exact = scale < 0x1p-100f || (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu;
+      const int64_t row = slot_row(a, slot[i]);
+      if (row < 0) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2)
+        w[e >> 1] = __nv_cvt_float2_to_fp8x2(make_float2(divide(x[i][e], scale, inv, exact), divide(x[i][e + 1], scale, inv, exact)),
+                                             __NV_SATFINITE, __NV_E4M3);
+      if (mine)
+        *reinterpret_cast<uint2*>(pool + row + (int64_t)h[i] * a.d + lane * 8) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+      if (lane == 0) a.scale[which][slot[i] * a.Hkv + h[i]] = scale;
+    }
+  }
+}
+
+// e4m3 pages of any d and alignment: one warp a (row, head), lane l holds
+// elements l, l + 32, ...
+template <typename S>
+__global__ void __launch_bounds__(256) append_e4m3_any_kernel(const AppendArgs a) {
   const int which = blockIdx.y, lane = threadIdx.x & 31;
   const S* src = static_cast<const S*>(a.src[which]);
   uint8_t* pool = static_cast<uint8_t*>(a.pool[which]);
@@ -268,12 +452,25 @@ int launch_page_append(const AppendArgs& a, int src_dtype, int kv_dtype, int sms
   const NvtxRange nvtx("dsa.page_append");
   const int64_t most = (int64_t)sms * 16;
   if (kv_dtype == DSA_DTYPE_FP8_E4M3) {
-    const int64_t rows = (int64_t)a.T * a.Hkv, blocks = (rows + 7) / 8;
-    const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);
-    if (src_dtype == DSA_DTYPE_FP32)
-      append_e4m3_kernel<float><<<grid, 256, 0, st>>>(a);
-    else
-      append_e4m3_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    const int64_t rows = (int64_t)a.T * a.Hkv;
+    const uintptr_t pools = reinterpret_cast<uintptr_t>(a.pool[0]) | reinterpret_cast<uintptr_t>(a.pool[1]);
+    if (a.d % 8 == 0 && a.page_stride % 8 == 0 && pools % 8 == 0 && rows < ((int64_t)1 << 31)) {
+      int lanes = 1;
+      while (lanes * 8 < a.d) lanes *= 2;
+      const int64_t at = 2 * (256 / lanes), blocks = (rows + at - 1) / at;
+      const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);
+      if (src_dtype == DSA_DTYPE_FP32)
+        append_e4m3_kernel<float><<<grid, 256, 0, st>>>(a, lanes);
+      else
+        append_e4m3_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, lanes);
+    } else {
+      const int64_t blocks = (rows + 7) / 8;
+      const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);
+      if (src_dtype == DSA_DTYPE_FP32)
+        append_e4m3_any_kernel<float><<<grid, 256, 0, st>>>(a);
+      else
+        append_e4m3_any_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+    }
   } else {
     const int elt = src_dtype == DSA_DTYPE_FP32 ? 4 : 2;
     const int64_t row_bytes = (int64_t)a.Hkv * a.d * elt;
@@ -282,7 +479,7 @@ int launch_page_append(const AppendArgs& a, int src_dtype, int kv_dtype, int sms
     const bool wide = row_bytes % 16 == 0 && a.page_stride * elt % 16 == 0 && pools % 16 == 0;
     const int vec = wide ? 16 : elt;
     const int units = (int)(row_bytes / vec);
-    const int64_t blocks = ((int64_t)a.T * units + 255) / 256;
+    const int64_t blocks = ((int64_t)a.T * ((units + 127) / 128) + 7) / 8;
     const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);
     if (wide)
       append_copy_kernel<uint4><<<grid, 256, 0, st>>>(a, units, 16 / elt);
