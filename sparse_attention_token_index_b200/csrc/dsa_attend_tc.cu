@@ -29,12 +29,16 @@
 //     four for the rest.
 //
 // The reference m is not the running maximum but one that no score has
-// passed by more than 2^8: as long as that holds no sum needs rescaling, and
-// whether it holds is one vote a tile.  When it fails (always in the first
-// tile) the rows' true maxima become the new reference and O and the row
-// sums are scaled once.  Weights lie in [0, 2^8], and their bf16 rounding
-// (2^-8 relative) is the same as for weights in [0, 1]; row sums are fp32
-// sums of the unrounded weights.
+// passed by more than 2^16: as long as that holds no sum needs rescaling, and
+// whether it holds is one vote a tile, taken behind the exponentials.  When
+// it fails (always in the first tile) the rows' true maxima become the new
+// reference, and O and the row sums are scaled once.  Weights lie in
+// [0, 2^16]; floating point keeps their bf16 rounding (half a step, 2^-8 of
+// the weight) and the fp32 sums of the unrounded weights as exact
+// as in [0, 1].  With tokens on the lanes a thread sees many rows, and their
+// references come from shared memory, where the copies queue; so the rows
+// share one, in a register, while no row's maximum is below it by more than
+// 2^64 (fp32 and bf16 hold 2^-126), and have their own beyond that.
 //
 // The work (all tiles of all requests and key heads, end to end) is cut into
 // equal runs, one per CTA, wherever the cuts fall: ragged batches and single
@@ -51,7 +55,8 @@ constexpr int kTile = 128;           // tokens a tile
 constexpr int kSoftWarps = 8, kLookWarps = 3, kCopyWarps = 16;
 constexpr int kWarps = kSoftWarps + 1 + kLookWarps + kCopyWarps;
 constexpr float kNoMax = -1.7e38f;   // reference of a row that has seen no token
-constexpr float kSlack = 8.f;        // log2 of the largest weight
+constexpr float kSlack = 16.f;       // log2 of the largest weight
+constexpr float kSpread = 64.f;      // log2 of the largest weight of a row that shares its reference, at least 2^-this
 
 struct TcAttend {
   AttendArgs a;
@@ -425,6 +430,8 @@ struct AttendSmem {
   uint64_t o_full[2], o_free[2], tok_full[kTok], tok_empty[kTok], drain;
   float red[2][4][N / 2 > 32 ? 32 : N / 2];
   alignas(16) float nref[N];
+  float rowmax[N], cref[2];
+  int common[2];
   float fac[N], lsum[2][N];
   int lim[N], orow[2][N];
   int64_t sums[32];
@@ -652,8 +659,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       constexpr int kQUnits = D / 8;
 #pragma unroll 2
       for (int e = lw * 32 + lane; e < N * kQUnits; e += kLookWarps * 32) {
-        const int r = e / kQUnits, u = e % kQUnits, rr = s.row0 + r, j = rr / g;
-        const bool in = r < s.rows && u * 8 < a.d;
+        const int r = e / kQUnits, u = e % kQUnits;
+        // rows behind the last repeat the first, so that their scores move no reference
+        const int rr = s.row0 + (r < s.rows ? r : 0), j = rr / g;
+        const bool in = u * 8 < a.d;
         const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
         uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
         if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
@@ -1101,13 +1110,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (tid < kC) {
           const int r = c0 + tid, rr = s.row0 + r, j = rr / g;
           S.nref[r] = -kNoMax;
-          S.lim[r] = kSel ? 0 : s.lim0 + j;
+          S.rowmax[r] = kNoMax;
+          S.lim[r] = kSel ? 0 : s.lim0 + (r < s.rows ? j : s.row0 / g);
           S.orow[seg & 1][r] = r < s.rows ? (s.q0 + j) * a.Hq + s.hk * g + (rr - j * g) : -1;
         }
         named_bar(bar, 128);
         float2 l[kC / 2];
 #pragma unroll
         for (int i = 0; i < kC / 2; ++i) l[i] = make_float2(0.f, 0.f);
+        bool common = true;   // one reference for this half's rows
+        float cref = -kNoMax;  // it, negated
         for (int j = 0; j < s.tiles; ++j, ++n) {
           const int tile = s.tile0 + j, tk = n % kTok;
           if constexpr (kSel || kFp8) ok = ok && mbar_wait(&S.tok_full[tk], (n / kTok) & 1, abort_flag, a.status, 94, budget);
@@ -1136,22 +1148,56 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           auto scores = [&]() {  // log2 weights against the references
             tmem_ld<kC>(col, x);
             tmem_ld_wait();
+            if (common) {
 #pragma unroll
-            for (int i = 0; i < kC; i += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(&S.nref[c0 + i]);
-              const float2 u = fma2(make_float2(x[i], x[i + 1]), make_float2(cs, cs), make_float2(m.x, m.y));
-              const float2 v = fma2(make_float2(x[i + 2], x[i + 3]), make_float2(cs, cs), make_float2(m.z, m.w));
-              x[i] = u.x;
-              x[i + 1] = u.y;
-              x[i + 2] = v.x;
-              x[i + 3] = v.y;
+              for (int i = 0; i < kC; i += 2) {
+                const float2 u = fma2(make_float2(x[i], x[i + 1]), make_float2(cs, cs), make_float2(cref, cref));
+                x[i] = u.x;
+                x[i + 1] = u.y;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kC; i += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&S.nref[c0 + i]);
+                x[i] = fmaf(x[i], cs, m.x);
+                x[i + 1] = fmaf(x[i + 1], cs, m.y);
+                x[i + 2] = fmaf(x[i + 2], cs, m.z);
+                x[i + 3] = fmaf(x[i + 3], cs, m.w);
+              }
             }
             hide();
           };
-          scores();
-          float top = fmaxf(x[0], x[1]);
+          uint8_t* prow = S.p[n & 1] + p_off;
+          const float vs = kFp8 ? S.vsc[tk][kFp8 ? key : 0] : 1.f;
+          auto put_weights = [&]() {
 #pragma unroll
-          for (int i = 2; i < kC; i += 2) top = fmaxf(fmaxf(top, x[i]), x[i + 1]);
+            for (int i = 0; i < kC; i += 8) {
+              uint32_t b[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                b[e] = kFp8 ? pack_bf16(x[i + 2 * e] * vs, x[i + 2 * e + 1] * vs) : pack_bf16(x[i + 2 * e], x[i + 2 * e + 1]);
+              *reinterpret_cast<uint4*>(prow + (((p_unit + (i >> 3)) ^ p_sw) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+          };
+          // One pass on the chance that no reference moves.  If one must, what
+          // the pass left is either right against the old reference or, where
+          // that was none or too far below, dropped.  P's buffer is free: the
+          // scores just read were multiplied after the weights of tile n - 2.
+          scores();
+          float top = x[0], top2 = x[1];
+#pragma unroll
+          for (int i = 2; i < kC; i += 2) {
+            top = fmaxf(top, x[i]);
+            top2 = fmaxf(top2, x[i + 1]);
+          }
+          top = fmaxf(top, top2);
+#pragma unroll
+          for (int i = 0; i < kC; i += 2) {
+            x[i] = ex2(x[i]);
+            x[i + 1] = ex2(x[i + 1]);
+            l[i >> 1] = add2(l[i >> 1], make_float2(x[i], x[i + 1]));
+          }
+          put_weights();
           if (bar_or(bar, 128, top > kSlack || !ok)) {
             if (bar_or(bar, 128, !ok)) {
               ok = false;
@@ -1166,20 +1212,37 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const float m = warp_columns<kC, true>(x);
             if (lane < kC) S.red[wg][wq][lane] = m;
             named_bar(bar, 128);
-            if (tid < kC) {
-              const float old = -S.nref[c0 + tid];
-              float mm = old;
+            if (wq == 0) {
+              const int r = c0 + lane % kC;
+              const float old = -S.nref[r];
+              float tile_max = S.red[wg][0][lane % kC];
 #pragma unroll
-              for (int w = 0; w < 4; ++w) mm = fmaxf(mm, S.red[wg][w][tid]);
-              S.nref[c0 + tid] = -mm;
-              S.fac[c0 + tid] = ex2(old - mm);
+              for (int w = 1; w < 4; ++w) tile_max = fmaxf(tile_max, S.red[wg][w][lane % kC]);
+              const float row_max = fmaxf(S.rowmax[r], tile_max), own = fmaxf(old, tile_max);
+              float hi = own, lo = row_max <= kNoMax ? INFINITY : row_max;
+#pragma unroll
+              for (int w = 16; w > 0; w >>= 1) {
+                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, w));
+                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, w));
+              }
+              // one for all while no row's best is too far below it
+              const bool one = common && lo >= hi - kSpread;
+              const float ref = one ? hi : own;
+              __syncwarp();
+              if (lane < kC) {
+                S.rowmax[r] = row_max;
+                S.nref[r] = -ref;
+                // a jump that the weights just summed may not have held: 2^-96 of what stood before is nothing beside them
+                S.fac[r] = ref - old > 96.f ? 0.f : ex2(old - ref);
+              }
+              if (lane == 0) {
+                S.common[wg] = one;
+                S.cref[wg] = -hi;
+              }
             }
             named_bar(bar, 128);
-#pragma unroll
-            for (int i = 0; i < kC / 2; ++i) {
-              l[i].x *= S.fac[c0 + 2 * i];
-              l[i].y *= S.fac[c0 + 2 * i + 1];
-            }
+            common = S.common[wg] != 0;
+            cref = S.cref[wg];
             if (j > 0) {  // the output tile holds the tiles before: wait for the last of them, then scale
               ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 91, budget);
               ok = __all_sync(0xffffffffu, ok);
@@ -1198,20 +1261,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               tmem_st_wait();
             }
             scores();
-          }
-          // P's buffer is free: the scores just read were multiplied after the weights of tile n - 2
-          uint8_t* prow = S.p[n & 1] + p_off;
-          const float vs = kFp8 ? S.vsc[tk][kFp8 ? key : 0] : 1.f;
 #pragma unroll
-          for (int i = 0; i < kC; i += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 u = make_float2(ex2(x[i + e]), ex2(x[i + e + 1]));
-              l[(i + e) >> 1] = add2(l[(i + e) >> 1], u);
-              w[e >> 1] = kFp8 ? pack_bf16(u.x * vs, u.y * vs) : pack_bf16(u.x, u.y);
+            for (int i = 0; i < kC; i += 2) {
+              x[i] = ex2(x[i]);
+              x[i + 1] = ex2(x[i + 1]);
+              const float f0 = S.fac[c0 + i], f1 = S.fac[c0 + i + 1];
+              float2& u = l[i >> 1];  // it holds this tile already
+              u.x = f0 > 0.f ? u.x * f0 : x[i];
+              u.y = f1 > 0.f ? u.y * f1 : x[i + 1];
             }
-            *reinterpret_cast<uint4*>(prow + (((p_unit + (i >> 3)) ^ p_sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            put_weights();
           }
           fence_async_smem();
           tc_fence_before();
@@ -1220,13 +1279,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mbar_arrive(&S.p_full[n & 1]);
             if constexpr (kSel || kFp8) mbar_arrive(&S.tok_empty[tk]);
           }
-          if (j == 0) store_output();
+          if (j == 1) store_output();  // of the segment before: its products are done
         }
         // ---- the segment's sums ----
         if (bar_or(bar, 128, !ok)) {
           ok = false;
           break;
         }
+        store_output();  // if this segment had one tile only
         pend = true;
         pend_whole = s.tiles == s.unit_tiles;
         pend_part = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
@@ -1249,7 +1309,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
           for (int w = 0; w < 4; ++w) sum += S.red[wg][w][tid];
           if (!pend_whole) {
-            a.part_ml[(pend_part * N + r) * 2] = -S.nref[r];
+            // a row without tokens here says so: it may share a reference far above its own scores elsewhere
+            a.part_ml[(pend_part * N + r) * 2] = sum > 0.f ? -S.nref[r] : kNoMax;
             a.part_ml[(pend_part * N + r) * 2 + 1] = sum;
           } else if (a.lse != nullptr && S.orow[pend_par][r] >= 0) {
             a.lse[S.orow[pend_par][r]] = sum > 0.f ? (log2f(sum) - S.nref[r]) * 0.693147181f : -INFINITY;
