@@ -3,13 +3,16 @@
 //
 // General kernel.  o = sum_s p_s v_s / sum_s p_s with p_s = exp(c q.k_s - m),
 // m the running maximum: one pass over the keys, the old sums scaled by
-// exp(m_old - m_new) whenever m grows.  A block of four warps takes one
-// (query row, head) and one part of the keys the row sees; each warp steps
-// through its share 32 keys at a time (a lane looks up one key's slot), and a
-// lane holds d / 32 elements of q and of the sums.  All fp32: it serves fp32
-// queries, where the weights' bf16 rounding of the tensor-core kernel would
-// not do, and head sizes that kernel has no tiles for.  Few rows are split
-// over the keys, and a second kernel joins the parts.
+// exp(m_old - m_new) whenever m grows.  A warp takes one (query row, head) and
+// steps through its keys 32 at a time (a lane looks up one key's slot); eight
+// lanes share a key, an eighth of the head each, so a key costs two wide loads
+// a lane and three shuffles, and the warp's four groups of lanes keep a few
+// keys each in flight; their sums are joined at the end.  All fp32: it serves
+// fp32 queries, where the weights' bf16 rounding of the tensor-core kernel
+// would not do, and the head sizes and alignments that kernel has no tiles
+// for.  Four warps share a row when rows are few (then also split over blocks,
+// whose parts a second kernel joins).  Gathered rows come from L2: 2048 rows of
+// 4 heads of 64, 64 entries each, read 268 MB of a 4 MB cache in 28 us.
 #include <cmath>
 
 #include "dsa_paged.cuh"
@@ -24,30 +27,64 @@ __device__ __forceinline__ float to_f32(uint8_t x) { return e4m3_to_f32(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-template <typename TQ, typename TK, int kD>  // kD: elements of the head a lane holds
+// This lane's eighth of a row: elements e + i of each vector of kE, zero
+// behind d.  kVec: rows start on the vectors' alignment and d holds whole ones.
+template <typename T, int kD, bool kVec>
+__device__ __forceinline__ void load_eighth(const T* row, int sub, int d, float (&x)[kD]) {
+  constexpr int kE = 16 / (int)sizeof(T) < kD ? 16 / (int)sizeof(T) : kD;
+#pragma unroll
+  for (int u = 0; u < kD / kE; ++u) {
+    const int e = (u * 8 + sub) * kE;
+    if constexpr (kVec) {
+      struct alignas(sizeof(T) * kE) Vec { T v[kE]; } v;
+      if (e < d) {
+        v = *reinterpret_cast<const Vec*>(row + e);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) x[u * kE + i] = to_f32(v.v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) x[u * kE + i] = 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) x[u * kE + i] = e + i < d ? to_f32(row[e + i]) : 0.f;
+    }
+  }
+}
+
+// The element that x[i] of load_eighth holds.
+template <typename T, int kD>
+__device__ __forceinline__ int eighth_element(int i, int sub) {
+  constexpr int kE = 16 / (int)sizeof(T) < kD ? 16 / (int)sizeof(T) : kD;
+  return ((i / kE) * 8 + sub) * kE + i % kE;
+}
+
+// kD: elements of the head a lane holds (d <= 8 kD); kShare: warps a row.
+template <typename TQ, typename TK, int kD, bool kVec, int kShare>
 __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const AttendArgs a, int splits) {
-  const int64_t task = blockIdx.x;
+  constexpr int kKeys = kD <= 16 ? 2 : 1;  // keys in flight in a group of lanes
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = lane >> 3, sub = lane & 7;
+  const int64_t task = kShare == 1 ? (int64_t)blockIdx.x * kGenWarps + warp : blockIdx.x;
   const int split = (int)(task % splits);
   const int64_t rh = task / splits;
+  if (rh >= (int64_t)a.total_q * a.Hq) return;  // only with kShare == 1: no barrier below
   const int row = (int)(rh / a.Hq), h = (int)(rh % a.Hq), hk = h / (a.Hq / a.Hkv);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowSeq rs = find_row(a, row);
   if (rs.b < 0) return;  // padding: its outputs stay
   // entries this row scans: list entries, or the tokens up to its position
   const int n = a.idx != nullptr ? a.k : max(0, rs.pos + 1);
   const int chunk = (n + splits - 1) / splits;
   const int n0 = min(n, split * chunk), n1 = min(n, n0 + chunk);
-  const TQ* q = static_cast<const TQ*>(a.Q) + ((int64_t)row * a.Hq + h) * a.d;
   const TK* K = static_cast<const TK*>(a.K);
   const TK* V = static_cast<const TK*>(a.V);
-  float qv[kD], o[kD], m = -INFINITY, l = 0.f;
+  float q[kD], o[kD], m = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < kD; ++i) {
-    const int e = lane + 32 * i;
-    qv[i] = e < a.d ? to_f32(q[e]) * a.scale : 0.f;
+  for (int i = 0; i < kD; ++i) {  // in the keys' order of elements
+    const int e = eighth_element<TK, kD>(i, sub);
+    q[i] = e < a.d ? to_f32(static_cast<const TQ*>(a.Q)[rh * a.d + e]) * a.scale : 0.f;
     o[i] = 0.f;
   }
-  for (int s0 = n0 + warp * 32; s0 < n1; s0 += kGenWarps * 32) {
+  for (int s0 = n0 + (kShare == 1 ? 0 : warp * 32); s0 < n1; s0 += kShare * 32) {
     // this lane's key: element offset of its row, -1 when it is skipped
     int64_t at = -1;
     float ks = 1.f, vs = 1.f;
@@ -67,87 +104,111 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
       }
     }
     const int cnt = min(32, n1 - s0);
-    for (int j0 = 0; j0 < cnt; j0 += 4) {
-      float s[4];
-      int64_t p[4];
+    for (int j0 = 0; j0 < cnt; j0 += 4 * kKeys) {  // key j0 + 4 i + grp
+      float s[kKeys], kv[kKeys][kD], w[kKeys];
+      int64_t p[kKeys];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        p[j] = __shfl_sync(0xffffffffu, at, j0 + j);
-        float dot = 0.f;
-        if (p[j] >= 0) {
-#pragma unroll
-          for (int i = 0; i < kD; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.d) dot = fmaf(qv[i], to_f32(K[p[j] + e]), dot);
-          }
-        }
-        s[j] = dot;
+      for (int i = 0; i < kKeys; ++i) {
+        p[i] = __shfl_sync(0xffffffffu, at, (j0 + 4 * i + grp) & 31);
+        if (j0 + 4 * i + grp >= cnt) p[i] = -1;
+        if (p[i] >= 0) load_eighth<TK, kD, kVec>(K + p[i], sub, a.d, kv[i]);
       }
 #pragma unroll
-      for (int w = 16; w > 0; w >>= 1)
+      for (int i = 0; i < kKeys; ++i) {
+        float dot = 0.f;
+        if (p[i] >= 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] += __shfl_xor_sync(0xffffffffu, s[j], w);
+          for (int e = 0; e < kD; ++e) dot = fmaf(q[e], kv[i][e], dot);
+          load_eighth<TK, kD, kVec>(V + p[i], sub, a.d, kv[i]);
+        }
+        s[i] = dot;
+      }
+#pragma unroll
+      for (int x = 4; x > 0; x >>= 1)
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
       float top = m;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[j] = p[j] >= 0 ? s[j] * __shfl_sync(0xffffffffu, ks, j0 + j) : -INFINITY;
-        top = fmaxf(top, s[j]);
+      for (int i = 0; i < kKeys; ++i) {
+        const float k = __shfl_sync(0xffffffffu, ks, (j0 + 4 * i + grp) & 31);
+        w[i] = __shfl_sync(0xffffffffu, vs, (j0 + 4 * i + grp) & 31);
+        s[i] = p[i] >= 0 ? s[i] * k : -INFINITY;
+        top = fmaxf(top, s[i]);
       }
-      if (top == -INFINITY) continue;  // nothing seen yet (the same on every lane)
-      const float keep = expf(m - top);
-      m = top;
-      l *= keep;
+      if (top == -INFINITY) continue;  // nothing seen yet (the same in the group's lanes)
+      if (top > m) {
+        const float keep = expf(m - top);
+        m = top;
+        l *= keep;
 #pragma unroll
-      for (int i = 0; i < kD; ++i) o[i] *= keep;
+        for (int e = 0; e < kD; ++e) o[e] *= keep;
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (p[j] < 0) continue;
-        const float w = expf(s[j] - m);
-        l += w;
-        const float wv = w * __shfl_sync(0xffffffffu, vs, j0 + j);
+      for (int i = 0; i < kKeys; ++i) {
+        if (p[i] < 0) continue;
+        const float x = expf(s[i] - m), xv = x * w[i];
+        l += x;
 #pragma unroll
-        for (int i = 0; i < kD; ++i) {
-          const int e = lane + 32 * i;
-          if (e < a.d) o[i] = fmaf(wv, to_f32(V[p[j] + e]), o[i]);
-        }
+        for (int e = 0; e < kD; ++e) o[e] = fmaf(xv, kv[i][e], o[e]);
       }
     }
   }
-  // the warps' parts, joined in warp order
-  __shared__ float so[kGenWarps][kD * 32], sm[kGenWarps], sl[kGenWarps];
+  // the groups' sums, joined pairwise
 #pragma unroll
-  for (int i = 0; i < kD; ++i) so[warp][lane + 32 * i] = o[i];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+  for (int x = 8; x <= 16; x <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, x), l2 = __shfl_xor_sync(0xffffffffu, l, x), top = fmaxf(m, m2);
+    const float f = m == -INFINITY ? 0.f : expf(m - top), f2 = m2 == -INFINITY ? 0.f : expf(m2 - top);
+    m = top;
+    l = l * f + l2 * f2;
+#pragma unroll
+    for (int e = 0; e < kD; ++e) o[e] = o[e] * f + __shfl_xor_sync(0xffffffffu, o[e], x) * f2;
   }
-  __syncthreads();
-  float top = sm[0];
+  if constexpr (kShare > 1) {  // the warps' parts, joined in warp order
+    __shared__ float so[kShare][kD * 8], sm[kShare], sl[kShare];
+    if (grp == 0) {
 #pragma unroll
-  for (int w = 1; w < kGenWarps; ++w) top = fmaxf(top, sm[w]);
-  float f[kGenWarps], sum = 0.f;
+      for (int i = 0; i < kD; ++i) so[warp][i * 8 + sub] = o[i];
+    }
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    float top = sm[0];
 #pragma unroll
-  for (int w = 0; w < kGenWarps; ++w) {
-    f[w] = sm[w] == -INFINITY ? 0.f : expf(sm[w] - top);
-    sum = fmaf(f[w], sl[w], sum);
+    for (int w = 1; w < kShare; ++w) top = fmaxf(top, sm[w]);
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kD; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) {
+      const float f = sm[w] == -INFINITY ? 0.f : expf(sm[w] - top);
+      l = fmaf(f, sl[w], l);
+#pragma unroll
+      for (int i = 0; i < kD; ++i) o[i] = fmaf(f, so[w][i * 8 + sub], o[i]);
+    }
+    m = top;
   }
   const bool last = splits == 1;
-  const float inv = last ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-  for (int e = threadIdx.x; e < a.d; e += kGenWarps * 32) {
-    float x = 0.f;
+  const float inv = last ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+  if (grp == 0) {
 #pragma unroll
-    for (int w = 0; w < kGenWarps; ++w) x = fmaf(f[w], so[w][e], x);
-    if (last)
-      put(static_cast<TQ*>(a.out) + rh * a.d + e, x * inv);
-    else
-      a.part_o[task * a.d + e] = x;
+    for (int i = 0; i < kD; ++i) {
+      const int e = eighth_element<TK, kD>(i, sub);
+      if (e >= a.d) continue;
+      if (last)
+        put(static_cast<TQ*>(a.out) + rh * a.d + e, o[i] * inv);
+      else
+        a.part_o[task * a.d + e] = o[i];
+    }
   }
-  if (threadIdx.x == 0) {
+  if (lane == 0) {
     if (last) {
-      if (a.lse != nullptr) a.lse[rh] = sum > 0.f ? top + logf(sum) : -INFINITY;
+      if (a.lse != nullptr) a.lse[rh] = l > 0.f ? m + logf(l) : -INFINITY;
     } else {
-      a.part_ml[2 * task] = top;
-      a.part_ml[2 * task + 1] = sum;
+      a.part_ml[2 * task] = m;
+      a.part_ml[2 * task + 1] = l;
     }
   }
 }
@@ -174,15 +235,32 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, in
   if (lane == 0 && a.lse != nullptr) a.lse[rh] = sum > 0.f ? top + logf(sum) : -INFINITY;
 }
 
-template <typename TQ, typename TK>
-static int run_general(const AttendArgs& a, int splits, cudaStream_t st) {
-  const unsigned grid = (unsigned)((int64_t)a.total_q * a.Hq * splits);
-  if (a.d <= 64)
-    attend_general_kernel<TQ, TK, 2><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
-  else if (a.d <= 128)
-    attend_general_kernel<TQ, TK, 4><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+template <typename TQ, typename TK, int kD>
+static void run_general(const AttendArgs& a, int splits, bool share, cudaStream_t st) {
+  constexpr int kE = 16 / (int)sizeof(TK) < kD ? 16 / (int)sizeof(TK) : kD;
+  constexpr uintptr_t kBytes = kE * sizeof(TK);
+  const bool vec = a.d % kE == 0 && a.page_stride % kE == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.K) | reinterpret_cast<uintptr_t>(a.V)) % kBytes == 0;
+  const int64_t tasks = (int64_t)a.total_q * a.Hq * splits;
+  const unsigned grid = (unsigned)(share ? tasks : (tasks + kGenWarps - 1) / kGenWarps);
+  if (share && vec)
+    attend_general_kernel<TQ, TK, kD, true, kGenWarps><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+  else if (share)
+    attend_general_kernel<TQ, TK, kD, false, kGenWarps><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+  else if (vec)
+    attend_general_kernel<TQ, TK, kD, true, 1><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
   else
-    attend_general_kernel<TQ, TK, 8><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+    attend_general_kernel<TQ, TK, kD, false, 1><<<grid, kGenWarps * 32, 0, st>>>(a, splits);
+}
+
+template <typename TQ, typename TK>
+static int run_general(const AttendArgs& a, int splits, bool share, cudaStream_t st) {
+  if (a.d <= 64)
+    run_general<TQ, TK, 8>(a, splits, share, st);
+  else if (a.d <= 128)
+    run_general<TQ, TK, 16>(a, splits, share, st);
+  else
+    run_general<TQ, TK, 32>(a, splits, share, st);
   if (splits > 1) {
     const int64_t rh = (int64_t)a.total_q * a.Hq;
     attend_join_kernel<TQ><<<(unsigned)((rh + 3) / 4), 128, 0, st>>>(a, splits);
@@ -190,11 +268,11 @@ static int run_general(const AttendArgs& a, int splits, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, cudaStream_t st) {
+int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, bool share, cudaStream_t st) {
   const NvtxRange nvtx(a.idx != nullptr ? "dsa.attend_selected" : "dsa.attend_paged");
-  if (q_dtype == DSA_DTYPE_FP32) return run_general<float, float>(a, splits, st);
-  if (kv_dtype == DSA_DTYPE_BF16) return run_general<__nv_bfloat16, __nv_bfloat16>(a, splits, st);
-  return run_general<__nv_bfloat16, uint8_t>(a, splits, st);
+  if (q_dtype == DSA_DTYPE_FP32) return run_general<float, float>(a, splits, share, st);
+  if (kv_dtype == DSA_DTYPE_BF16) return run_general<__nv_bfloat16, __nv_bfloat16>(a, splits, share, st);
+  return run_general<__nv_bfloat16, uint8_t>(a, splits, share, st);
 }
 
 }  // namespace dsa
@@ -207,10 +285,16 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// A (row, head) has a warp to itself when that makes 16 warps a
+// multiprocessor, and four warps otherwise: 2048 rows of 4 heads, 64 entries
+// each, take 28 us so and 65 us with four.
+bool general_share(int sms, int total_q, int Hq) { return (int64_t)total_q * Hq < (int64_t)sms * 16; }
+
 // Parts of the keys a (row, head) is split into: enough blocks for eight a
 // multiprocessor, at most 64.
 int general_splits(int sms, int total_q, int Hq) {
   const int64_t tasks = (int64_t)total_q * Hq, want = (int64_t)sms * 8;
+  if (!general_share(sms, total_q, Hq)) return 1;
   const int64_t s = (want + tasks - 1) / tasks;
   return (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
 }
@@ -297,7 +381,8 @@ int attend(AttendArgs& a, const float* softmax_scale, int q_dtype, int kv_dtype,
   const AttendPlan p = plan_general(sms, a.total_q, a.Hq, a.d);
   a.part_ml = reinterpret_cast<float*>(ws + p.ml_off);
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
-  return launch_attend_general(a, q_dtype, kv_dtype, p.splits, static_cast<cudaStream_t>(stream));
+  return launch_attend_general(a, q_dtype, kv_dtype, p.splits, general_share(sms, a.total_q, a.Hq),
+                               static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace

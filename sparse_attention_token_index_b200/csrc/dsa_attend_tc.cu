@@ -422,7 +422,7 @@ struct AttendSmem {
   uint8_t q[C::kQBufs][C::kQBytes];
   uint8_t p[2][C::kPBytes ? C::kPBytes : 16];
   float ksc[kTok][kFp8 ? kTile : 4], vsc[kTok][kFp8 ? kTile : 4];
-  int rows[kTok][kTile];
+  alignas(16) int rows[kTok][kTile];
   uint32_t seen[kTok][4];
   uint64_t full[C::kSlots], empty[C::kSlots];
   uint64_t q_full[2], q_empty[2];
@@ -576,13 +576,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (!ok || S.rows[n % kTok][0] == kEnd) break;
         const int r = slot_free(n);
         if (!ok) break;
-        const int* rows = S.rows[n % kTok] + row0 + sub;
-        const uint32_t dst = smem_u32(S.ring[r]) + (unit >> 3) * kTile * 128 + (row0 + sub) * 128;
+        int rows[kTimes];  // a group of lanes copies consecutive rows: their numbers come in wide loads
+#pragma unroll
+        for (int i = 0; i < kTimes; i += 4)
+          *reinterpret_cast<int4*>(rows + i) = *reinterpret_cast<const int4*>(&S.rows[n % kTok][row0 + sub * kTimes + i]);
+        const uint32_t dst = smem_u32(S.ring[r]) + (unit >> 3) * kTile * 128 + (row0 + sub * kTimes) * 128;
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
-          const int row = rows[i * kRowsAt];
+          const int row = rows[i];
           const bool in = row >= 0 && unit_ok;
-          copy16(dst + i * kRowsAt * 128 + (((unit & 7) ^ ((i * kRowsAt + sub) & 7)) << 4),
+          copy16(dst + i * 128 + (((unit & 7) ^ ((sub * kTimes + i) & 7)) << 4),
                  in ? pages + (uint64_t)(uint32_t)row * row_bytes : static_cast<const uint8_t*>(a.K), in);
         }
         copies_arrive(&S.full[r]);

@@ -81,8 +81,9 @@ __device__ __forceinline__ int page_of(const AttendArgs& a, int b, int pos, int&
   return id;
 }
 
-// The general CUDA-core attention (dsa_attend.cu): `splits` parts a row.
-int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, cudaStream_t st);
+// The general CUDA-core attention (dsa_attend.cu): `splits` parts a row; a
+// block or (without `share`) a warp each.
+int launch_attend_general(const AttendArgs& a, int q_dtype, int kv_dtype, int splits, bool share, cudaStream_t st);
 
 // The tensor-core attention (dsa_attend_tc.cu): whether it takes a call, and
 // its workspace, for at most `rows` query rows that read the same cache.

@@ -321,19 +321,20 @@ __device__ __forceinline__ int64_t slot_row(const AppendArgs& a, int64_t slot) {
 template <typename V>
 __global__ void __launch_bounds__(256) append_copy_kernel(const AppendArgs a, int units, int per_vec) {
   constexpr int kAt = 4;
-  const int which = blockIdx.y, lane = threadIdx.x & 31, parts = (units + 32 * kAt - 1) / (32 * kAt);
+  const bool second = blockIdx.y != 0;
+  const int lane = threadIdx.x & 31, parts = (units + 32 * kAt - 1) / (32 * kAt);
   const int64_t n = (int64_t)a.T * parts, step = (int64_t)gridDim.x * 8;
   for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < n; w += step) {
     const int64_t t = parts == 1 ? w : w / parts;
     const int u0 = (int)(w - t * parts) * 32 * kAt + lane;
-    const V* src = static_cast<const V*>(a.src[which]) + t * units;
+    const V* src = static_cast<const V*>(second ? a.src[1] : a.src[0]) + t * units;
     V x[kAt];
 #pragma unroll
     for (int i = 0; i < kAt; ++i)
       if (u0 + 32 * i < units) x[i] = src[u0 + 32 * i];
     const int64_t row = slot_row(a, a.slots[t]);
     if (row < 0) continue;
-    V* dst = static_cast<V*>(a.pool[which]) + row / per_vec;
+    V* dst = static_cast<V*>(second ? a.pool[1] : a.pool[0]) + row / per_vec;
 #pragma unroll
     for (int i = 0; i < kAt; ++i)
       if (u0 + 32 * i < units) dst[u0 + 32 * i] = x[i];
@@ -364,19 +365,23 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
   }
 }
 
-// e4m3 pages, d a multiple of 8 and rows on 8 bytes: `lanes` (a power of two)
-// a (row, head), eight elements a lane, two rows in flight.  32768 rows of 8
-// heads of 128, bf16: 204 MB.
-template <typename S>
+// e4m3 pages, d a multiple of kE (8 or 16) and rows on kE bytes: `lanes` (a
+// power of two) a (row, head), kE elements a lane, 16 in flight.  What a row
+// costs beside its elements (slot, reductions, scale) is shared by more of
+// them with 16 a lane: 32768 rows of 8 heads of 128, K and V, 204 MB, take
+// 46 us (31 us at the copy bandwidth), and 74 us with 8 a lane.
+template <typename S, int kE>
 __global__ void __launch_bounds__(256) append_e4m3_kernel(const AppendArgs a, int lanes) {
-  constexpr int kAt = 2;
-  const int which = blockIdx.y, lane = threadIdx.x & (lanes - 1);
-  const S* src = static_cast<const S*>(a.src[which]);
-  uint8_t* pool = static_cast<uint8_t*>(a.pool[which]);
+  constexpr int kAt = kE == 16 ? 1 : 2;
+  const bool second = blockIdx.y != 0;
+  const int lane = threadIdx.x & (lanes - 1);
+  const S* src = static_cast<const S*>(second ? a.src[1] : a.src[0]);
+  uint8_t* pool = static_cast<uint8_t*>(second ? a.pool[1] : a.pool[0]);
+  float* scales = second ? a.scale[1] : a.scale[0];
   const int n = a.T * a.Hkv, per_block = 256 / lanes;  // fewer than 2^31 rows (host)
-  const bool mine = lane * 8 < a.d;
+  const bool mine = lane * kE < a.d;
   for (int64_t r0 = (int64_t)blockIdx.x * kAt * per_block; r0 < n; r0 += (int64_t)gridDim.x * kAt * per_block) {
-    float x[kAt][8];
+    float x[kAt][kE];
     int64_t slot[kAt];
     int h[kAt];
 #pragma unroll
@@ -385,34 +390,60 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(const AppendArgs a, in
       slot[i] = -1;
       h[i] = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      for (int e = 0; e < kE; ++e) x[i][e] = 0.f;
       if (r < n) {
         const int t = (int)((unsigned)r / (unsigned)a.Hkv);
         h[i] = (int)r - t * a.Hkv;
         slot[i] = a.slots[t];
-        if (mine) load8(src + r * a.d + lane * 8, x[i]);
+        if (mine) {
+#pragma unroll
+          for (int e = 0; e < kE; e += 8) load8(src + r * a.d + lane * kE + e, *reinterpret_cast<float(*)[8]>(&x[i][e]));
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
       float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(x[i][e]));
       for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float scale = fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f), inv = __frcp_rn(scale);
-      const bool exact = scale < 0x1p-100f || (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu;
+      const float scale = fmaxf(divide(top, 448.f, 1.f / 448.f, false), 1.17549435e-38f), inv = __frcp_rn(scale);
       const int64_t row = slot_row(a, slot[i]);
       if (row < 0) continue;
-      uint32_t w[4];
+      if (scale < 0x1p-100f || (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2)
-        w[e >> 1] = __nv_cvt_float2_to_fp8x2(make_float2(divide(x[i][e], scale, inv, exact), divide(x[i][e + 1], scale, inv, exact)),
-                                             __NV_SATFINITE, __NV_E4M3);
-      if (mine)
-        *reinterpret_cast<uint2*>(pool + row + (int64_t)h[i] * a.d + lane * 8) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-      if (lane == 0) a.scale[which][slot[i] * a.Hkv + h[i]] = scale;
+        for (int e = 0; e < kE; ++e) x[i][e] = divide(x[i][e], scale, inv, true);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) x[i][e] = divide(x[i][e], scale, inv, false);
+      }
+      uint32_t w[kE / 4];
+#pragma unroll
+      for (int e = 0; e < kE; e += 4)
+        w[e >> 2] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[i][e], x[i][e + 1]), __NV_SATFINITE, __NV_E4M3) |
+                    (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[i][e + 2], x[i][e + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+      uint8_t* dst = pool + row + (int64_t)h[i] * a.d + lane * kE;
+      if constexpr (kE == 16) {
+        if (mine) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        if (mine) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      }
+      if (lane == 0) scales[slot[i] * a.Hkv + h[i]] = scale;
     }
   }
+}
+
+template <typename S>
+static void append_e4m3(const AppendArgs& a, int64_t rows, int64_t most, bool wide, cudaStream_t st) {
+  const int per = wide ? 16 : 8;
+  int lanes = 1;
+  while (lanes * per < a.d) lanes *= 2;
+  const int64_t at = (wide ? 1 : 2) * (256 / lanes), blocks = (rows + at - 1) / at;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);
+  if (wide)
+    append_e4m3_kernel<S, 16><<<grid, 256, 0, st>>>(a, lanes);
+  else
+    append_e4m3_kernel<S, 8><<<grid, 256, 0, st>>>(a, lanes);
 }
 
 // e4m3 pages of any d and alignment: one warp a (row, head), lane l holds
@@ -455,14 +486,11 @@ int launch_page_append(const AppendArgs& a, int src_dtype, int kv_dtype, int sms
     const int64_t rows = (int64_t)a.T * a.Hkv;
     const uintptr_t pools = reinterpret_cast<uintptr_t>(a.pool[0]) | reinterpret_cast<uintptr_t>(a.pool[1]);
     if (a.d % 8 == 0 && a.page_stride % 8 == 0 && pools % 8 == 0 && rows < ((int64_t)1 << 31)) {
-      int lanes = 1;
-      while (lanes * 8 < a.d) lanes *= 2;
-      const int64_t at = 2 * (256 / lanes), blocks = (rows + at - 1) / at;
-      const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);
+      const bool wide16 = a.d % 16 == 0 && a.page_stride % 16 == 0 && pools % 16 == 0;
       if (src_dtype == DSA_DTYPE_FP32)
-        append_e4m3_kernel<float><<<grid, 256, 0, st>>>(a, lanes);
+        append_e4m3<float>(a, rows, most, wide16, st);
       else
-        append_e4m3_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, lanes);
+        append_e4m3<__nv_bfloat16>(a, rows, most, wide16, st);
     } else {
       const int64_t blocks = (rows + 7) / 8;
       const dim3 grid((unsigned)(blocks < most ? blocks : most), a.n_src);

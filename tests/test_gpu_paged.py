@@ -456,3 +456,113 @@ def test_indexer_then_selected_attention(kv):
     q, w = torch.randn((512, 64, 128), device=DEV).bfloat16(), torch.rand((512, 64), device=DEV)
     s.idx, _ = dsa.dsa_index_dense(q, w, keys[:512], 256, q_pos0=0, check=True)
     _both(s)
+
+
+# ---------------------------------------------------------------------------
+# where the kernels change form
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("B,longest,new,page", [(2047, 40, 3, 16), (2048, 9, 1, 1), (2049, 40, 3, 16), (5000, 20, 2, 8)])
+def test_plan_of_many_requests(B, longest, new, page):
+    # one launch up to 2048 requests, two beyond; outputs apart from their inputs
+    lens, news, table, free, used, n_pages, mt = _plan_case(B, longest, new, page, seed=B)
+    got = _run_plan(lens, news, table, free, used, page, n_pages, mt)
+    _same_plan(got, P.page_plan(lens, news, table, free, used, page, mt))
+
+
+@pytest.mark.parametrize("src", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [128, 24, 7])  # 16, 8 and one element a lane
+def test_append_e4m3_rounds_as_the_division_does(src, d):
+    """The stored bytes are those of rn_e4m3(rn_fp32(x / scale)), at the borders between e4m3 values too: scales that
+    are powers of two, have a fraction of all ones, lie near the smallest normal number or are large."""
+    gen = torch.Generator().manual_seed(d)
+    half = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    mid = (half[1:] + half[:-1]) / 2  # the borders
+    scales = [1.0, 2.0 ** -20, 2.0 - 2.0 ** -23, (2.0 - 2.0 ** -23) * 2.0 ** -40, 1.17549435e-38, 2.0 ** -119, 3e35, 0.3]
+    rows = []
+    for s in scales:
+        for _ in range(8):
+            pick = mid[torch.randint(0, len(mid), (d,), generator=gen)]
+            x = pick * s * (1 + torch.randint(-2, 3, (d,), generator=gen).double() * 2.0 ** -23)
+            x *= torch.randint(0, 2, (d,), generator=gen).double() * 2 - 1
+            x[0] = 448.0 * s
+            rows.append(x)
+    x = torch.stack(rows).to(TYPES[src])[:, None].to(DEV)
+    T = x.shape[0]
+    K = torch.zeros((T, 1, 1, d), dtype=torch.float8_e4m3fn, device=DEV)
+    sc = torch.zeros((T, 1, 1), device=DEV)
+    dsa.dsa_page_append(x, K, torch.arange(T, device=DEV), K_scale=sc, check=True)
+    xf = x.cpu().float()[:, 0]
+    want_s = (xf.abs().amax(-1) / np.float32(448)).clamp(min=2.0 ** -126)
+    assert torch.equal(sc.cpu().view(-1), want_s)
+    want = (xf / want_s[:, None]).to(torch.float8_e4m3fn)
+    assert torch.equal(K.cpu().view(T, d).view(torch.uint8), want.view(torch.uint8))
+
+
+def _baselines(step, per_head, per_query):
+    """Gives every (query, head) row a baseline score of its own: keys share a direction that queries have more or less
+    of.  ``per_head`` and ``per_query`` are the amounts."""
+    d = step.d
+    k0 = torch.zeros(d)
+    k0[: d // 2] = 1.0
+    K = step.K.float()
+    K = torch.where(K.isnan(), K, K * 0.25 + k0.to(DEV)).to(step.K.dtype)
+    step.K.copy_(K)
+    rows, Hq = step.Q.shape[:2]
+    amount = torch.tensor([[per_head[h % len(per_head)] + per_query[r % len(per_query)] for h in range(Hq)]
+                           for r in range(rows)])
+    step.Q.copy_((step.Q.float().cpu() * 0.5 + amount[..., None] * k0).to(step.Q.dtype))
+
+
+@pytest.mark.parametrize("k", [None, 300])
+@pytest.mark.parametrize("Hq,Hkv,m", [(2, 1, 8), (8, 1, 4), (64, 1, 1), (64, 1, 2), (32, 8, 1)])
+def test_attend_rows_far_apart(Hq, Hkv, m, k):
+    # rows that share a tile have baselines hundreds of powers of two apart, and the last tile of a cut cache holds
+    # tokens that only the later queries see
+    step = Step([128 * 2 + m - 3, 128 * 6 + 1, 700], [m, m, m], Hq, Hkv, 128, "bf16", page=16, pad=2, k=k, seed=m + Hq)
+    _baselines(step, [0.0, 40.0, -40.0, 3.0], [0.0] * (m // 2) + [60.0] * (m - m // 2))
+    _both(step)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [None, 100])
+def test_attend_pages_off_16_bytes(kv, k):
+    step = Step([300, 129], [2, 1], 8, 2, 128, kv, page=16, k=k)
+    for name in ("K", "V"):
+        x = getattr(step, name)
+        buf = torch.empty(x.numel() + 1, dtype=x.dtype, device=DEV)
+        buf[1:] = x.reshape(-1)
+        setattr(step, name, buf[1:].view(x.shape))
+    _both(step)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_cache_of_more_than_2_to_the_32_bytes(kv):
+    # 2^20 + 64 pages of 16 tokens, 2 heads of 128: the last pages lie beyond 2^32 elements
+    n_pages, page, Hkv, d, Hq = (1 << 20) + 64, 16, 2, 128, 8
+    small = Step([500, 40], [1, 2], Hq, Hkv, d, kv, page=page, k=64)
+    dt = TYPES[kv]
+    big = [torch.empty((n_pages, page, Hkv, d), dtype=dt, device=DEV) for _ in range(2)]
+    scales = [torch.empty((n_pages, page, Hkv), device=DEV) if kv == "e4m3" else None for _ in range(2)]
+    have = small.K.shape[0]
+    for x, b, s, bs in zip((small.K, small.V), big, small.scales, scales):
+        b.view(torch.uint8)[-have:] = x.view(torch.uint8)
+        if s is not None:
+            bs[-have:] = s
+    want = [dsa.dsa_attend_paged(*small.args(), small.max_q, **small.scale_args()),
+            dsa.dsa_attend_selected(*small.args(), small.idx, **small.scale_args())]
+    table = torch.where(small.table >= 0, small.table + (n_pages - have), small.table)
+    args = (small.Q, big[0], big[1], table, small.lens_t, small.q_off)
+    sc = {"K_scale": scales[0], "V_scale": scales[1]}
+    assert torch.equal(dsa.dsa_attend_paged(*args, small.max_q, check=True, **sc), want[0])
+    assert torch.equal(dsa.dsa_attend_selected(*args, small.idx, check=True, **sc), want[1])
+    # and written there
+    rows = torch.randn((3, Hkv, d), device=DEV).to(torch.bfloat16)
+    slots = torch.tensor([n_pages * page - 1, 5, n_pages * page - 17], device=DEV)
+    dsa.dsa_page_append(rows, big[0], slots, v=rows, V_pages=big[1], check=True, **sc)
+    at = (slots // page, slots % page)
+    got = big[0].view(torch.uint8)[at[0], at[1]].view(dt).float()
+    if kv == "e4m3":
+        got = got * scales[0][at[0], at[1]][..., None]
+        assert torch.all((got - rows.float()).abs() <= 2.0 ** -4 * rows.float().abs() + scales[0][at[0], at[1]][..., None] * 2.0 ** -9)
+    else:
+        assert torch.equal(got, rows.float())
