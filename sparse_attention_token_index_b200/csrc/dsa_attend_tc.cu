@@ -33,9 +33,20 @@
 // whether it holds is one vote a tile, taken behind the exponentials.  When
 // it fails (always in the first tile) the rows' true maxima become the new
 // reference, and O and the row sums are scaled once.  Weights lie in
-// [0, 2^16]; floating point keeps their bf16 rounding (half a step, 2^-8 of
-// the weight) and the fp32 sums of the unrounded weights as exact
-// as in [0, 1].  With tokens on the lanes a thread sees many rows, and their
+// [0, 2^16], where floating point is as exact as in [0, 1].
+//
+// The matrix unit takes weights in bf16.  One rounding (2^-8 of a weight at
+// most) would leave outputs 1.4 times as far off as their own rounding to bf16
+// does.  Up to 32 rows each weight goes in as two, its bf16 and the bf16 of what
+// that left (2^-16 together): the rests are N more columns of the same product,
+// which waits for A's bytes from shared memory and takes no longer for it up
+// to 64 columns.  With more rows that costs a quarter of the time (32 caches of
+// 131072 tokens, 128 rows each: 473 us for 366), and the weights are rounded
+// once; the output is divided by the sum of the rounded weights, which leaves
+// rows of few tokens exact.  (e4m3 weights carry V's scales and are always
+// split.)  The log-sum-exp comes from the fp32 sum of the weights themselves.
+//
+// With tokens on the lanes a thread sees many rows, and their
 // references come from shared memory, where the copies queue; so the rows
 // share one, in a register, while no row's maximum is below it by more than
 // 2^64 (fp32 and bf16 hold 2^-126), and have their own beyond that.
@@ -300,9 +311,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// Two fp32 -> two bf16, and the bf16 of what those left of them: the sum of
+// both is within 2^-17 of the value.
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x0, x1);
+  const float2 h = unpack_bf16(hi), r = add2(make_float2(x0, x1), make_float2(-h.x, -h.y));
+  lo = pack_bf16(r.x, r.y);
 }
 
 // Four e4m3 bytes -> four bf16, exactly, in the order 0, 2, 1, 3: sign,
@@ -396,22 +418,27 @@ struct Cfg {
   static constexpr int kSlotBytes = kTile * D * 2;   // one K or V tile, bf16
   static constexpr int kQBytes = N * D * 2;
   static constexpr int kQBufs = 2;
-  static constexpr int kPBytes = kRows ? 0 : N * kTile * 2;
-  static constexpr int kPRow = N >= 64 ? 128 : N * 2;  // bytes of a P row
-  static constexpr int kOther = kQBufs * kQBytes + 2 * kPBytes + (kFp8 ? kTok * kTile * 8 : 0);
+  static constexpr bool kSplit = kFp8 || N <= 32;    // weights go in as two bf16
+  static constexpr int kPCols = kSplit ? 2 * N : N;
+  static constexpr int kPBufs = kSplit && N >= 64 ? 1 : 2;
+  static constexpr int kPBytes = kRows ? 0 : kPCols * kTile * 2;
+  static constexpr int kPRow = kPCols >= 64 ? 128 : kPCols * 2;  // bytes of a P row (of its first 64 columns)
+  static constexpr int kOther = kQBufs * kQBytes + kPBufs * kPBytes + (kFp8 ? kTok * kTile * 8 : 0);
   static constexpr int kBudget = 232448 - 1024 - 10240;
   static constexpr int kFit = (kBudget - kOther) / kSlotBytes;
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   // Registers a thread: launched with 72 (28 warps), of which the copy warps
   // give some up, so that the softmax warps hold a row's or token's scores.
   // 256 x kSoftRegs + 128 x kMidRegs + 512 x kCopyRegs <= 896 x 72.
-  static constexpr int kSoftRegs = 128, kMidRegs = kFp8 ? 56 : 72, kCopyRegs = kFp8 ? 48 : 40;
+  static constexpr int kSoftRegs = kFp8 ? 128 : 144, kMidRegs = 56, kCopyRegs = kFp8 ? 48 : 40;
   static_assert(256 * kSoftRegs + 128 * kMidRegs + 512 * kCopyRegs <= kWarps * 32 * 72, "the registers of the launch");
-  // tensor memory: two score tiles, with rows on the lanes two tiles of bf16
-  // weights, and two output tiles (one where no more fit)
-  static constexpr int kSCols = N, kPCol = 2 * N, kOCol = kRows ? 2 * N + 128 : 2 * N, kOCols = kRows ? D : N;
+  // Tensor memory: two score tiles; with rows on the lanes the weights, two
+  // tiles or one and its rests (64 columns each); two output tiles, one where
+  // no more fit (tokens on the lanes: the columns of the rests are added when
+  // it is stored).
+  static constexpr int kSCols = N, kPCol = 2 * N, kOCol = kRows ? 2 * N + 128 : 2 * N, kOCols = kRows ? D : kPCols;
   static constexpr int kOBufs = kRows && D == 128 ? 1 : 2;
-  static constexpr int kCols = N == 128 ? 512 : 4 * N;
+  static constexpr int kCols = N >= 64 ? 512 : 8 * N;
   static_assert(kSlots >= 2, "the ring holds a K and a V tile");
 };
 
@@ -420,7 +447,7 @@ struct AttendSmem {
   using C = Cfg<N, D, kFp8>;
   uint8_t ring[C::kSlots][C::kSlotBytes];
   uint8_t q[C::kQBufs][C::kQBytes];
-  uint8_t p[2][C::kPBytes ? C::kPBytes : 16];
+  uint8_t p[C::kPBufs][C::kPBytes ? C::kPBytes : 16];
   float ksc[kTok][kFp8 ? kTile : 4], vsc[kTok][kFp8 ? kTile : 4];
   alignas(16) int rows[kTok][kTile];
   uint32_t seen[kTok][4];
@@ -429,6 +456,7 @@ struct AttendSmem {
   uint64_t s_full[2], p_full[2], p_empty[2];
   uint64_t o_full[2], o_free[2], tok_full[kTok], tok_empty[kTok], drain;
   float red[2][4][N / 2 > 32 ? 32 : N / 2];
+  float sum[2][2][C::kRows ? N : 1], red2[2][4][N == 64 && C::kSplit == false ? 32 : 1];
   alignas(16) float nref[N];
   float rowmax[N], cref[2];
   int common[2];
@@ -760,7 +788,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     Seg s;
     constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
     constexpr uint32_t kIdescO = C::kRows ? idesc_bf16_f32(128, D) | (1u << 16)                // V along N
-                                          : idesc_bf16_f32(D, N) | (1u << 15) | (1u << 16);  // V^T along M, P along N
+                                          : idesc_bf16_f32(D, C::kPCols) | (1u << 15) | (1u << 16);  // V^T along M, P along N
     const bool leader = elect_one();
     const uint64_t kdesc = sw128_kmajor_desc(smem_u32(S.ring[0])), vdesc = mnmajor_desc<128>(smem_u32(S.ring[0]), kTile * 128);
     const uint64_t qdesc = sw128_kmajor_desc(smem_u32(S.q[0])), pdesc = mnmajor_desc<C::kPRow>(smem_u32(S.p[0]), kTile * 128);
@@ -782,16 +810,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       tc_fence_after();
       if (leader) {
         const uint64_t v = vdesc + (uint64_t)(pend_slot * (C::kSlotBytes >> 4));
-        const uint64_t p = pdesc + (uint64_t)(pb * (C::kPBytes >> 4));
-        const uint32_t o = tmem_base + C::kOCol + par * C::kOCols, ps = tmem_base + C::kPCol + pb * 64;
+        const uint64_t p = pdesc + (uint64_t)(i % C::kPBufs * (C::kPBytes >> 4));
+        const uint32_t o = tmem_base + C::kOCol + par * C::kOCols, ps = tmem_base + C::kPCol + (C::kPBufs == 2 ? pb * 64 : 0);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k) {
-          if constexpr (C::kRows)
-            tc_mma_bf16_ts(o, ps + k * 8, v + (uint64_t)(k * (2048 >> 4)), kIdescO,
-                           !(pend_first && k == 0));
-          else
-            tc_mma_bf16(o, v + (uint64_t)(k * (2048 >> 4)), p + (uint64_t)(k * C::kPRow), kIdescO,
-                        !(pend_first && k == 0));
+          const uint64_t vk = v + (uint64_t)(k * (2048 >> 4));
+          if constexpr (C::kRows) {
+            tc_mma_bf16_ts(o, ps + k * 8, vk, kIdescO, !(pend_first && k == 0));
+            if constexpr (C::kSplit) tc_mma_bf16_ts(o, ps + 64 + k * 8, vk, kIdescO, 1);
+          } else {
+            tc_mma_bf16(o, vk, p + (uint64_t)(k * C::kPRow), kIdescO, !(pend_first && k == 0));
+          }
         }
         tc_commit(&S.empty[pend_slot]);
         tc_commit(&S.p_empty[pb]);
@@ -921,7 +950,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const int rr = s.row0 + r, jq = rr / g;
         const int orow = r < s.rows ? (s.q0 + jq) * a.Hq + s.hk * g + (rr - jq * g) : -1;
         const int lim = kSel ? 0x7fffffff : s.lim0 + jq;
-        float nref = -kNoMax, l = 0.f;
+        float nref = -kNoMax, l = 0.f, lr = 0.f;  // sums of the weights, and of their bf16
         for (int j = 0; j < s.tiles; ++j, ++n) {
           const int tile = s.tile0 + j, tk = n % kTok;
           if constexpr (kSel || kFp8) ok = ok && mbar_wait(&S.tok_full[tk], (n / kTok) & 1, abort_flag, a.status, 94, budget);
@@ -988,6 +1017,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const float fac = ex2(-nref - m);
             nref = -m;
             l *= fac;
+            lr *= fac;
             if (j > 0) {  // the output tile holds the tiles before: wait for the last of them, then scale
               ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 91, budget);
               ok = __all_sync(0xffffffffu, ok);
@@ -1008,28 +1038,43 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
             for (int i = 0; i < 64; ++i) x[i] += nref;
           }
-          // the weights' tile is free: the scores just read were multiplied after the weights of tile n - 2
-          const uint32_t pcol = tmem_base + lanes + (uint32_t)(C::kPCol + (n & 1) * 64 + wg * 32);
           float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i0 = 0; i0 < 64; i0 += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              float2 u = make_float2(ex2(x[i0 + i]), ex2(x[i0 + i + 1])), v = make_float2(ex2(x[i0 + i + 2]), ex2(x[i0 + i + 3]));
-              l2 = add2(l2, add2(u, v));
-              if constexpr (kFp8) {
-                const float4 vs = *reinterpret_cast<const float4*>(&S.vsc[tk][c0 + i0 + i]);
-                u.x *= vs.x;
-                u.y *= vs.y;
-                v.x *= vs.z;
-                v.y *= vs.w;
-              }
-              w[i >> 1] = pack_bf16(u.x, u.y);
-              w[(i >> 1) + 1] = pack_bf16(v.x, v.y);
-            }
-            tmem_st8(pcol + (i0 >> 1), w);
+          for (int i = 0; i < 64; i += 4) {
+            const float2 u = make_float2(ex2(x[i]), ex2(x[i + 1])), v = make_float2(ex2(x[i + 2]), ex2(x[i + 3]));
+            l2 = add2(l2, add2(u, v));
+            float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
+            if constexpr (kFp8) vs = *reinterpret_cast<const float4*>(&S.vsc[tk][c0 + i]);
+            x[i] = u.x * vs.x;
+            x[i + 1] = u.y * vs.y;
+            x[i + 2] = v.x * vs.z;
+            x[i + 3] = v.y * vs.w;
           }
+          // the weights' tile: two, the scores just read were multiplied after
+          // the weights of tile n - 2; one, free once those of tile n - 1 are
+          if (C::kPBufs == 1 && n > 0) {
+            ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 92, budget);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+          }
+          const uint32_t pcol = tmem_base + lanes + (uint32_t)(C::kPCol + (C::kPBufs == 2 ? (n & 1) * 64 : 0) + wg * 32);
+          float2 r2 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i0 = 0; i0 < 64; i0 += 16) {
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (C::kSplit) {
+                split_bf16(x[i0 + 2 * i], x[i0 + 2 * i + 1], hi[i], lo[i]);
+              } else {
+                hi[i] = pack_bf16(x[i0 + 2 * i], x[i0 + 2 * i + 1]);
+                r2 = add2(r2, unpack_bf16(hi[i]));
+              }
+            }
+            tmem_st8(pcol + (i0 >> 1), hi);
+            if constexpr (C::kSplit) tmem_st8(pcol + 64 + (i0 >> 1), lo);
+          }
+          lr += r2.x + r2.y;
           l += l2.x + l2.y;
           tmem_st_wait();
           tc_fence_before();
@@ -1045,20 +1090,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           ok = false;
           break;
         }
-        (&S.red[0][0][0])[wg * 128 + r] = l;
+        S.sum[wg][0][r] = l;
+        S.sum[wg][1][r] = lr;
         named_bar(bar, kGroup);
-        const float sum = (&S.red[0][0][0])[r] + (&S.red[0][0][0])[128 + r];
+        const float sum = S.sum[0][0][r] + S.sum[1][0][r];
+        const float rounded = C::kSplit ? sum : S.sum[0][1][r] + S.sum[1][1][r];
         pend = true;
         pend_whole = s.tiles == s.unit_tiles;
         pend_part = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
         pend_par = seg % C::kOBufs;
         pend_phase = (seg / C::kOBufs) & 1;
         pend_row = orow;
-        pend_inv = sum > 0.f ? 1.f / sum : 0.f;
+        pend_inv = rounded > 0.f ? 1.f / rounded : 0.f;
         if (wg == 0) {
           if (!pend_whole) {
-            a.part_ml[(pend_part * N + r) * 2] = -nref;
-            a.part_ml[(pend_part * N + r) * 2 + 1] = sum;
+            reinterpret_cast<float4*>(a.part_ml)[pend_part * N + r] = make_float4(-nref, sum, rounded, 0.f);
           } else if (a.lse != nullptr && orow >= 0) {
             a.lse[orow] = sum > 0.f ? (log2f(sum) - nref) * 0.693147181f : -INFINITY;
           }
@@ -1073,6 +1119,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const int key = wq * 32 + lane, c0 = wg * kC;
       // this thread's P row: 16-byte units swizzled over the row's width
       const uint32_t p_off = (uint32_t)(key * C::kPRow), p_unit = wg * (kC / 8);
+      // the rests: behind all rows' weights, with 64 rows in the next 64 columns
+      constexpr uint32_t kRest = N == 64 ? kTile * 128 : 0, kRestUnit = N == 64 ? 0 : N / 8;
       const uint32_t p_sw = C::kPRow == 128 ? key & 7 : (C::kPRow == 64 ? (key >> 1) & 3 : (key >> 2) & 1);
       // 128 rows of O^T fill the 128 lanes; 64 fill the first 16 lanes of each warp
       const int dv = element(D == 128 ? wq * 32 + lane : wq * 16 + lane);
@@ -1086,7 +1134,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const uint32_t o = tmem_base + lanes + (uint32_t)(C::kOCol + pend_par * C::kOCols + c0);
         float v[kC];
         tmem_ld<kC>(o, v);
-        tmem_ld_wait();
+        if constexpr (C::kSplit) {
+          float rest[kC];
+          tmem_ld<kC>(o + N, rest);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kC; ++i) v[i] += rest[i];
+        } else {
+          tmem_ld_wait();
+        }
         if (ok && dv_ok) {
           if (!pend_whole) {
             float* dst = a.part_o + (pend_part * N + c0) * D + dv;
@@ -1118,9 +1174,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           S.orow[seg & 1][r] = r < s.rows ? (s.q0 + j) * a.Hq + s.hk * g + (rr - j * g) : -1;
         }
         named_bar(bar, 128);
-        float2 l[kC / 2];
+        constexpr int kL = C::kSplit ? 1 : kC / 2;
+        float2 l[kC / 2], lr[kL];  // sums of the weights, and of their bf16
 #pragma unroll
         for (int i = 0; i < kC / 2; ++i) l[i] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kL; ++i) lr[i] = make_float2(0.f, 0.f);
         bool common = true;   // one reference for this half's rows
         float cref = -kNoMax;  // it, negated
         for (int j = 0; j < s.tiles; ++j, ++n) {
@@ -1170,22 +1229,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             }
             hide();
           };
-          uint8_t* prow = S.p[n & 1] + p_off;
+          uint8_t* prow = S.p[n % C::kPBufs] + p_off;
           const float vs = kFp8 ? S.vsc[tk][kFp8 ? key : 0] : 1.f;
-          auto put_weights = [&]() {
+          auto put_weights = [&](auto add) {  // and adds them to the sums
 #pragma unroll
             for (int i = 0; i < kC; i += 8) {
-              uint32_t b[4];
+              uint32_t hi[4];
+              [[maybe_unused]] uint32_t lo[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                b[e] = kFp8 ? pack_bf16(x[i + 2 * e] * vs, x[i + 2 * e + 1] * vs) : pack_bf16(x[i + 2 * e], x[i + 2 * e + 1]);
-              *reinterpret_cast<uint4*>(prow + (((p_unit + (i >> 3)) ^ p_sw) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
+              for (int e = 0; e < 4; ++e) {
+                const float w0 = x[i + 2 * e], w1 = x[i + 2 * e + 1];
+                add(l[i / 2 + e], i + 2 * e, make_float2(w0, w1));
+                if constexpr (C::kSplit) {
+                  split_bf16(kFp8 ? w0 * vs : w0, kFp8 ? w1 * vs : w1, hi[e], lo[e]);
+                } else {
+                  hi[e] = pack_bf16(w0, w1);
+                  add(lr[i / 2 + e], i + 2 * e, unpack_bf16(hi[e]));
+                }
+              }
+              const uint32_t u = p_unit + (i >> 3);
+              *reinterpret_cast<uint4*>(prow + ((u ^ p_sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              if constexpr (C::kSplit)
+                *reinterpret_cast<uint4*>(prow + kRest + (((u + kRestUnit) ^ p_sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
           };
           // One pass on the chance that no reference moves.  If one must, what
           // the pass left is either right against the old reference or, where
-          // that was none or too far below, dropped.  P's buffer is free: the
-          // scores just read were multiplied after the weights of tile n - 2.
+          // that was none or too far below, dropped.
           scores();
           float top = x[0], top2 = x[1];
 #pragma unroll
@@ -1195,12 +1265,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           }
           top = fmaxf(top, top2);
 #pragma unroll
-          for (int i = 0; i < kC; i += 2) {
-            x[i] = ex2(x[i]);
-            x[i + 1] = ex2(x[i + 1]);
-            l[i >> 1] = add2(l[i >> 1], make_float2(x[i], x[i + 1]));
+          for (int i = 0; i < kC; ++i) x[i] = ex2(x[i]);
+          // P's buffer: two, the scores just read were multiplied after the
+          // weights of tile n - 2; one, free once those of tile n - 1 are
+          if (C::kPBufs == 1 && n > 0) {
+            ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 92, budget);
+            ok = __all_sync(0xffffffffu, ok);
           }
-          put_weights();
+          put_weights([](float2& u, int, float2 w) { u = add2(u, w); });
           if (bar_or(bar, 128, top > kSlack || !ok)) {
             if (bar_or(bar, 128, !ok)) {
               ok = false;
@@ -1253,27 +1325,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               const uint32_t o = tmem_base + lanes + (uint32_t)(C::kOCol + (seg & 1) * C::kOCols + c0);
 #pragma unroll
               for (int i0 = 0; i0 < kC; i0 += 8) {
-                float v[8];
-                uint32_t w[8];
-                tmem_ld<8>(o + i0, v);
-                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i] * S.fac[c0 + i0 + i]);
-                tmem_st8(o + i0, w);
+                for (int rest = 0; rest < 2; ++rest) {
+                  float v[8];
+                  uint32_t w[8];
+                  tmem_ld<8>(o + rest * N + i0, v);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i] * S.fac[c0 + i0 + i]);
+                  tmem_st8(o + rest * N + i0, w);
+                }
               }
               tmem_st_wait();
             }
             scores();
 #pragma unroll
-            for (int i = 0; i < kC; i += 2) {
-              x[i] = ex2(x[i]);
-              x[i + 1] = ex2(x[i + 1]);
-              const float f0 = S.fac[c0 + i], f1 = S.fac[c0 + i + 1];
-              float2& u = l[i >> 1];  // it holds this tile already
-              u.x = f0 > 0.f ? u.x * f0 : x[i];
-              u.y = f1 > 0.f ? u.y * f1 : x[i + 1];
-            }
-            put_weights();
+            for (int i = 0; i < kC; ++i) x[i] = ex2(x[i]);
+            put_weights([&](float2& u, int c, float2 w) {  // the sums hold this tile already
+              const float f0 = S.fac[c0 + c], f1 = S.fac[c0 + c + 1];
+              u.x = f0 > 0.f ? u.x * f0 : w.x;
+              u.y = f1 > 0.f ? u.y * f1 : w.y;
+            });
           }
           fence_async_smem();
           tc_fence_before();
@@ -1304,21 +1376,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           }
           const float sum = warp_columns<kC, false>(v);
           if (lane < kC) S.red[wg][wq][lane] = sum;
+          if constexpr (!C::kSplit) {
+#pragma unroll
+            for (int i = 0; i < kC / 2; ++i) {
+              v[2 * i] = lr[i].x;
+              v[2 * i + 1] = lr[i].y;
+            }
+            const float rounded = warp_columns<kC, false>(v);
+            if (lane < kC) S.red2[wg][wq][lane] = rounded;
+          }
         }
         named_bar(bar, 128);
         if (tid < kC) {
           const int r = c0 + tid;
-          float sum = 0.f;
+          float sum = 0.f, rounded = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) sum += S.red[wg][w][tid];
+          if constexpr (!C::kSplit) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) rounded += S.red2[wg][w][tid];
+          } else {
+            rounded = sum;
+          }
           if (!pend_whole) {
             // a row without tokens here says so: it may share a reference far above its own scores elsewhere
-            a.part_ml[(pend_part * N + r) * 2] = sum > 0.f ? -S.nref[r] : kNoMax;
-            a.part_ml[(pend_part * N + r) * 2 + 1] = sum;
+            reinterpret_cast<float4*>(a.part_ml)[pend_part * N + r] =
+                make_float4(sum > 0.f ? -S.nref[r] : kNoMax, sum, rounded, 0.f);
           } else if (a.lse != nullptr && S.orow[pend_par][r] >= 0) {
             a.lse[S.orow[pend_par][r]] = sum > 0.f ? (log2f(sum) - S.nref[r]) * 0.693147181f : -INFINITY;
           }
-          S.lsum[pend_par][r] = sum > 0.f ? 1.f / sum : 0.f;
+          S.lsum[pend_par][r] = rounded > 0.f ? 1.f / rounded : 0.f;
         }
         named_bar(bar, 128);  // the rows' state is free for the next segment
         ++seg;
@@ -1344,7 +1431,7 @@ template <int N, int D>
 __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a, const JoinDesc* desc) {
   constexpr int kRows = 4, kPer = D / 32;
   __shared__ float so[8][kRows][D];
-  __shared__ float sm[8][kRows], sl[8][kRows];
+  __shared__ float sm[8][kRows], sl[8][kRows], sr[8][kRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const JoinDesc d = desc[c];
@@ -1355,11 +1442,11 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a,
   const int parts = (int)(c1 - c0) + 1;
   // parts: the end of run c0 (its only segment, or its last), then the beginnings of the others
   const int64_t slot0 = d.first == c0 * d.run ? 2 * c0 : 2 * c0 + 1;
-  float m[kRows], l[kRows], o[kRows][kPer];
+  float m[kRows], l[kRows], lr[kRows], o[kRows][kPer];
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     m[r] = kNoMax;
-    l[r] = 0.f;
+    l[r] = lr[r] = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) o[r][i] = 0.f;
   }
@@ -1368,13 +1455,15 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a,
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int64_t row = slot * N + r0 + r;
-      const float pm = a.part_ml[row * 2], pl = a.part_ml[row * 2 + 1];
+      const float4 ml = reinterpret_cast<const float4*>(a.part_ml)[row];
+      const float pm = ml.x;
       float v[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] = a.part_o[row * D + lane + 32 * i];
       const float top = fmaxf(m[r], pm), f = ex2(m[r] - top), pf = ex2(pm - top);
       m[r] = top;
-      l[r] = l[r] * f + pl * pf;
+      l[r] = l[r] * f + ml.y * pf;
+      lr[r] = lr[r] * f + ml.z * pf;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) o[r][i] = o[r][i] * f + v[i] * pf;
     }
@@ -1386,15 +1475,19 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a,
     if (lane == 0) {
       sm[warp][r] = m[r];
       sl[warp][r] = l[r];
+      sr[warp][r] = lr[r];
     }
   }
   __syncthreads();
   const int r = warp;  // one warp a row
   if (r >= kRows || r0 + r >= d.rows) return;
-  float top = kNoMax, sum = 0.f;
+  float top = kNoMax, sum = 0.f, rounded = 0.f;
   for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w][r]);
-  for (int w = 0; w < 8; ++w) sum = fmaf(ex2(sm[w][r] - top), sl[w][r], sum);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  for (int w = 0; w < 8; ++w) {
+    sum = fmaf(ex2(sm[w][r] - top), sl[w][r], sum);
+    rounded = fmaf(ex2(sm[w][r] - top), sr[w][r], rounded);
+  }
+  const float inv = rounded > 0.f ? 1.f / rounded : 0.f;
   const int g = a.Hq / a.Hkv, rr = d.row0 + r0 + r, j = rr / g;
   const int64_t orow = (int64_t)(d.q0 + j) * a.Hq + d.hk * g + (rr - j * g);
   for (int e = lane; e < a.d; e += 32) {
@@ -1417,7 +1510,7 @@ int attend_tc_rows(int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows
 size_t attend_tc_bytes(int sms, int rows, int d) {
   const int N = attend_tc_rows(rows);
   d = d > 64 ? 128 : 64;
-  return sizeof(WsHeader) + round256((size_t)sms * sizeof(JoinDesc)) + round256((size_t)sms * 2 * N * 8) +
+  return sizeof(WsHeader) + round256((size_t)sms * sizeof(JoinDesc)) + round256((size_t)sms * 2 * N * 16) +
          round256((size_t)sms * 2 * N * d * 4);
 }
 
@@ -1491,7 +1584,7 @@ int run_attend_tc(const AttendArgs& args, int kv_dtype, int rows, int sms, uint8
   t.desc = reinterpret_cast<JoinDesc*>(ws + off);
   off += round256((size_t)sms * sizeof(JoinDesc));
   t.a.part_ml = reinterpret_cast<float*>(ws + off);
-  off += round256((size_t)sms * 2 * N * 8);
+  off += round256((size_t)sms * 2 * N * 16);
   t.a.part_o = reinterpret_cast<float*>(ws + off);
   t.row_stride_page = (int)(args.page_stride / args.d);
   int grid = sms;
