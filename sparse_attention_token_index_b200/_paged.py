@@ -1,4 +1,9 @@
-"""ctypes binding of the paged-cache calls (``include/dsa_paged.h``; argument marshalling only)."""
+"""Binding of the paged-cache calls (``include/dsa_paged.h``; argument marshalling only).
+
+A plain call (on the current device and stream, outputs allocated here, with a
+workspace) goes through the ``_paged_ext`` extension; every other one, and any
+whose arguments do not pass, through the checks below and ctypes.
+"""
 from __future__ import annotations
 
 import contextlib
@@ -94,6 +99,22 @@ def _pool(K, V, K_scale, V_scale, device, Hkv, d) -> Tuple[int, int]:
 
 
 _same = contextlib.nullcontext()
+_EXT = None
+
+
+def _ext():
+    """The extension, bound to the loaded library; raises if it has not been built."""
+    global _EXT
+    if _EXT is None:
+        try:
+            from . import _paged_ext
+        except ImportError as e:
+            raise RuntimeError("the _paged_ext extension is missing or does not fit this torch: build it with "
+                               "`python -m sparse_attention_token_index_b200.build`") from e
+        L = lib()
+        _paged_ext.bind(*(ctypes.cast(getattr(L, n), _vp).value for n in EXPORTED_SYMBOLS))
+        _EXT = _paged_ext
+    return _EXT
 
 
 def _on(device: torch.device, stream):
@@ -162,6 +183,10 @@ def dsa_page_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     few free pages (DSA_ERR_PAGES) or lengths out of range fail as a whole:
     the table stays, the step has no tokens, and the status word tells.
     """
+    if out is None and stream is None and not check and workspace is not None:
+        r = (_EXT or _ext()).page_plan(lens, new_lens, block_table, free_pages, used, page, n_pages, max_tokens, workspace)
+        if r is not None:
+            return r if type(r) is tuple else _check(r, "dsa_page_plan")
     dev = lens.device
     if lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("lens must be [B], block_table [B, max_pages], free_pages [n_free]")
@@ -210,6 +235,10 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
     each token and head: scale = max(amax / 448, 2^-126).  ``v`` and
     ``V_pages`` may be left out (a cache of keys alone).
     """
+    if stream is None and not check and workspace is not None:
+        r = (_EXT or _ext()).page_append(k, K_pages, slots, v, V_pages, K_scale, V_scale, workspace)
+        if r is not None:
+            return _check(r, "dsa_page_append")
     if k.dim() != 3:
         raise ValueError("k must be [T, Hkv, d]")
     dev, shape = k.device, k.shape
@@ -236,6 +265,11 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
 
 def _attend(name, Q, K, V, block_table, lens, q_offsets, idx, max_q, scale, K_scale, V_scale, out, lse, workspace,
             stream, check):
+    if out is None and stream is None and not check and workspace is not None and (lse is None or lse is True):
+        r = (_EXT or _ext()).attend(Q, K, V, block_table, lens, q_offsets, idx, K_scale, V_scale, workspace, max_q, scale,
+                                    lse is True)
+        if r is not None:
+            return _check(r, name) if type(r) is int else r
     if Q.dim() != 3 or K.dim() != 4 or lens.dim() != 1 or block_table.dim() != 2 or (idx is not None and idx.dim() != 2):
         raise ValueError("Q must be [total_q, Hq, d], K_pages [n_pages, page, Hkv, d], lens [B], block_table "
                          "[B, max_pages], idx [total_q, k]")

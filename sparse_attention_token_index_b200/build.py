@@ -4,7 +4,9 @@ Usage: ``python -m sparse_attention_token_index_b200.build [--verbose] [--debug-
 Each ``csrc/*.cu`` is compiled with nvcc (``-gencode
 arch=compute_100a,code=sm_100a``) in parallel and linked into one shared
 library next to this file; the CUDA runtime is linked statically, so the
-library loads without a GPU (only calls into it need one).
+library loads without a GPU (only calls into it need one).  ``csrc/paged_ext.cpp``
+becomes ``_paged_ext.so``, the Python extension that hands torch tensors to the
+library's paged-cache calls.
 
 ``--debug-bounds`` builds ``libdsa_index_debug.so`` instead: the same
 library compiled with ``-DDSA_DEBUG_BOUNDS=1``, whose kernels check every
@@ -26,6 +28,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa_index.so")
 DEBUG_LIB = os.path.join(PKG, "libdsa_index_debug.so")
+EXT = os.path.join(PKG, "_paged_ext.so")
+EXT_SRC = os.path.join(CSRC, "paged_ext.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -59,7 +63,31 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def build_ext(force: bool = False) -> str:
+    """Compiles the Python extension against the installed torch."""
+    deps = [EXT_SRC, os.path.join(INCLUDE, "dsa_paged.h"), os.path.join(INCLUDE, "dsa_index.h"), __file__]
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in deps):
+        return EXT
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = EXT + ".tmp"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           "-I" + sysconfig.get_paths()["include"], f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
+           f"-I{cuda}/include", EXT_SRC, "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=None, debug_bounds: bool = False) -> str:
+    build_ext(force and not debug_bounds)
     lib = DEBUG_LIB if debug_bounds else LIB
     if not force and up_to_date(lib):
         return lib

@@ -566,3 +566,53 @@ def test_a_cache_of_more_than_2_to_the_32_bytes(kv):
         assert torch.all((got - rows.float()).abs() <= 2.0 ** -4 * rows.float().abs() + scales[0][at[0], at[1]][..., None] * 2.0 ** -9)
     else:
         assert torch.equal(got, rows.float())
+
+
+# ---------------------------------------------------------------------------
+# the two ways into the library
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "fp32"])
+def test_plain_calls_and_detailed_ones_agree(kv):
+    # with a workspace and nothing else of the caller's the extension makes the call; with `out` _paged.py does
+    ext = dsa._paged._ext()
+    step = Step([300, 7, 129], [2, 1, 3], 8, 2, 64, kv, k=50)
+    sc = step.scale_args()
+    ws = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
+    for idx, f in ((None, lambda **kw: dsa.dsa_attend_paged(*step.args(), step.max_q, scale=0.1, workspace=ws, **sc, **kw)),
+                   (step.idx, lambda **kw: dsa.dsa_attend_selected(*step.args(), step.idx, scale=0.1, workspace=ws, **sc, **kw))):
+        assert ext.attend(*step.args(), idx, sc["K_scale"], sc["V_scale"], ws, step.max_q, 0.1, False) is not None
+        o, l = f(return_lse=True)
+        o2, l2 = f(out=torch.empty_like(step.Q), lse=torch.empty_like(l))
+        assert torch.equal(o, o2) and torch.equal(l, l2) and torch.equal(f(), o)
+    rows = torch.randn((5, 2, 64), device=DEV).to(step.Q.dtype)
+    slots = torch.tensor([3, 1, -1, 40, 17], device=DEV)
+    pages = [[x.clone() for x in (step.K, step.V)] + [None if s is None else s.clone() for s in step.scales] for _ in range(2)]
+    for (K, V, ks, vs), kw in zip(pages, ({"workspace": ws}, {"check": True})):
+        dsa.dsa_page_append(rows, K, slots, v=rows, V_pages=V, K_scale=ks, V_scale=vs, **kw)
+    for x, y in zip(*pages):
+        assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    lens, news, table, free, used, n_pages, mt = _plan_case(9, 300, 5, 16, seed=2)
+    _same_plan(_run_plan(lens, news, table, free, used, 16, n_pages, mt, workspace=ws),
+               P.page_plan(lens, news, table, free, used, 16, mt))
+    dsa.dsa_check_status(ws)
+
+
+def test_the_extension_leaves_what_it_does_not_take():
+    ext = dsa._paged._ext()
+    step = Step([40, 9], [1, 2], 4, 2, 64, "bf16", k=8)
+    ws = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
+    good = [*step.args(), step.idx, None, None, ws, step.max_q, None, False]
+    assert ext.attend(*good) is not None
+    for i, bad in ((0, step.Q.half()), (0, step.Q[:, :, ::2]), (0, step.Q.cpu()), (1, step.K.float()), (1, step.K[:, :, :1]),
+                   (2, step.V[:, :5]), (3, step.table.long()), (3, step.table.t()), (4, step.lens_t[:1]), (5, step.lens_t),
+                   (6, step.idx.long()), (6, step.idx[:, ::2]), (7, torch.ones(3, device=DEV)), (9, ws[:16]), (9, None),
+                   (10, 1.5), (11, "1")):
+        assert ext.attend(*good[:i], bad, *good[i + 1:]) is None, i
+    with pytest.raises(TypeError):
+        dsa.dsa_attend_selected(step.Q.half(), *step.args()[1:], step.idx, workspace=ws)
+    with pytest.raises(ValueError, match="workspace"):
+        dsa.dsa_attend_selected(*step.args(), step.idx, workspace=ws[:16])
+    with pytest.raises(dsa.DsaError):  # the library's own refusal
+        dsa.dsa_attend_paged(*step.args(), 0, workspace=ws)
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_page_plan(step.lens_t, step.lens_t, step.table, step.lens_t, step.lens_t[:1], 0, 4, 8, workspace=ws)

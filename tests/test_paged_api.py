@@ -118,3 +118,18 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
         dsa.dsa_page_plan(t["lens"], t["lens"], t["table"], t["lens"], t["lens"][:1], 16, 4, 8)
     with pytest.raises(TypeError):
         dsa.dsa_page_plan(t["lens"].long(), t["lens"], t["table"], t["lens"], t["lens"][:1], 16, 4, 8)
+
+
+def test_the_extension_takes_no_cpu_tensors():
+    ext = dsa._paged._ext()
+    i = torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    assert ext.page_plan(i, i, torch.zeros((2, 4), dtype=torch.int32), i, i[:1], 16, 4, 8, ws) is None
+    k = torch.zeros((2, 2, 64))
+    assert ext.page_append(k, torch.zeros((1, 4, 2, 64)), i.long(), None, None, None, None, ws) is None
+    assert ext.attend(k, torch.zeros((1, 4, 2, 64)), torch.zeros((1, 4, 2, 64)), i[None], i[:1], i, None, None, None, ws, 1,
+                      None, True) is None
+    for f in (ext.page_plan, ext.page_append, ext.attend):
+        assert f() is None and f(1, 2) is None
+    with pytest.raises(TypeError):
+        ext.bind(1)
