@@ -131,7 +131,8 @@ __device__ __forceinline__ int64_t request_tiles(const AttendArgs& a, int b) {
   return sum * a.Hkv;
 }
 
-// Steps through the segments of a CTA's run; every role keeps its own.
+// Steps through the segments of a CTA's run; every role keeps its own, and
+// whole warps step.
 template <int N, bool kSel>
 struct Walk {
   int64_t left;  // tiles still to hand out
@@ -142,10 +143,10 @@ struct Walk {
   __device__ __forceinline__ void start(const TcAttend& t, int64_t n, int b_, int64_t off_) {
     left = n;
     if constexpr (kSel) {
-      const int64_t u = off_ / t.unit_tiles;
-      row = (int)(u / t.a.Hkv);
-      hk = (int)(u % t.a.Hkv);
-      off = (int)(off_ % t.unit_tiles);
+      const int64_t u = div64(off_, t.unit_tiles);
+      row = (int)div64(u, t.a.Hkv);
+      hk = (int)(u - (int64_t)row * t.a.Hkv);
+      off = (int)(off_ - u * t.unit_tiles);
       q0 = q1 = 0;
       b = 0;
     } else {
@@ -157,8 +158,8 @@ struct Walk {
         int end;
         const int g = t.a.Hq / t.a.Hkv, blocks = (m * g + N - 1) / N;
         for (int i = 0; i < blocks; ++i) per_head += block_tiles<N>(m, g, len, i, end);
-        hk = (int)(off_ / per_head);
-        int64_t o = off_ % per_head;
+        hk = (int)div64(off_, per_head);
+        int64_t o = off_ - hk * per_head;
         for (int n_t; o >= (n_t = block_tiles<N>(m, g, len, rb, end)); ++rb) o -= n_t;
         off = (int)o;
       }
@@ -534,12 +535,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     if (lane == 31) S.sums[warp] = inc;
     __syncthreads();
-    int64_t before = inc - mine, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += S.sums[w];
-      total += S.sums[w];
+    int64_t warps = lane < kWarps ? S.sums[lane] : 0;  // every warp adds up the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, warps, o);
+      if (lane >= o) warps += u;
     }
-    run = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t total = __shfl_sync(0xffffffffu, warps, 31);
+    const int64_t earlier = __shfl_sync(0xffffffffu, warps, warp > 0 ? warp - 1 : 0);
+    const int64_t before = inc - mine + (warp > 0 ? earlier : 0);
+    run = div64(total + gridDim.x - 1, gridDim.x);
     if (run < t.min_run) run = t.min_run;
     begin = (int64_t)blockIdx.x * run;
     if (begin >= before && begin < before + mine) {
@@ -556,27 +561,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   tc_fence_after();
   const uint32_t tmem_base = S.tmem_base;
   const int64_t n_tiles = max((int64_t)0, min(run, S.total - begin));
-  if (threadIdx.x == 0) {  // the join's description of the unit this run begins in
-    JoinDesc d;
-    d.rows = 0;
-    d.run = run;
-    d.first = d.last = begin;
-    d.q0 = d.hk = d.row0 = 0;
-    if (n_tiles > 0) {
-      Walk<N, kSel> w;
-      Seg s;
-      w.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
-      w.next(t, s);
-      d.rows = s.valid ? s.rows : 0;
-      d.first = begin - s.tile0;
-      d.last = d.first + s.unit_tiles;
-      d.q0 = s.q0;
-      d.hk = s.hk;
-      d.row0 = s.row0;
-    }
-    t.desc[blockIdx.x] = d;
-  }
-
   if (warp >= kSoftWarps + 1 + kLookWarps) {
     // ---------------- copy warps: cache rows -> ring ----------------
     set_regs<C::kCopyRegs, false>();
@@ -680,7 +664,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     };
     while (ok && walk.next(t, s)) {
       if (!s.valid) continue;
-      // the segment's queries, a third each
+      // the segment's queries, a third each; the first segment's by two warps, as the third looks up its first tile
+      const bool split3 = qn > 0;
       const int qb = qn % C::kQBufs;
       if (qn >= C::kQBufs)
         ok = mbar_wait<true>(&S.q_empty[qb], (qn / C::kQBufs - 1) & 1, abort_flag, a.status, 70, budget);
@@ -689,7 +674,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       const uint8_t* Q = static_cast<const uint8_t*>(a.Q);
       constexpr int kQUnits = D / 8;
 #pragma unroll 2
-      for (int e = lw * 32 + lane; e < N * kQUnits; e += kLookWarps * 32) {
+      for (int e = (split3 ? lw : (lw > 0 ? lw - 1 : N * kQUnits)) * 32 + lane; e < N * kQUnits;
+           e += (split3 ? kLookWarps : kLookWarps - 1) * 32) {
         const int r = e / kQUnits, u = e % kQUnits;
         // rows behind the last repeat the first, so that their scores move no reference
         const int rr = s.row0 + (r < s.rows ? r : 0), j = rr / g;
@@ -778,6 +764,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
         __syncwarp();
       }
+    }
+    if (lw == 0) {  // what the join needs of the unit this run begins in
+      JoinDesc d;
+      d.rows = 0;
+      d.run = run;
+      d.first = d.last = begin;
+      d.q0 = d.hk = d.row0 = 0;
+      if (n_tiles > 0) {
+        walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+        walk.next(t, s);
+        d.rows = s.valid ? s.rows : 0;
+        d.first = begin - s.tile0;
+        d.last = d.first + s.unit_tiles;
+        d.q0 = s.q0;
+        d.hk = s.hk;
+        d.row0 = s.row0;
+      }
+      if (lane == 0) t.desc[blockIdx.x] = d;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kMma) {
@@ -1424,78 +1428,100 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // ----------------------------------------------------------------------------
 // Joins the parts of the units that cuts between CTAs divide.  Block (c, y)
 // looks at the cut before CTA c and, if it is the first cut of its unit,
-// joins rows 4 y .. 4 y + 3: the warps share the parts, then meet in shared
-// memory in a fixed order.
+// joins rows 4 y .. 4 y + 3: a warp a row when the parts are few, else the
+// warps share the parts of all four and meet in shared memory, in a fixed
+// order.  It is all latency, so the loads of four parts are in flight at once.
 // ----------------------------------------------------------------------------
+template <int D>
+struct JoinSum {
+  static constexpr int kPer = D / 32;
+  float m = kNoMax, l = 0.f, lr = 0.f, o[kPer] = {};
+  __device__ __forceinline__ void add(float pm, float pl, float plr, const float (&v)[kPer]) {
+    const float top = fmaxf(m, pm), f = ex2(m - top), pf = ex2(pm - top);
+    m = top;
+    l = l * f + pl * pf;
+    lr = lr * f + plr * pf;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = o[i] * f + v[i] * pf;
+  }
+};
+
 template <int N, int D>
-__global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendArgs a, const JoinDesc* desc) {
+__global__ void __launch_bounds__(128) attend_tc_join_kernel(const AttendArgs a, const JoinDesc* desc) {
   constexpr int kRows = 4, kPer = D / 32;
-  __shared__ float so[8][kRows][D];
-  __shared__ float sm[8][kRows], sl[8][kRows], sr[8][kRows];
+  __shared__ float so[4][kRows][D], sm[4][kRows][3];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const JoinDesc d = desc[c];
   const int r0 = blockIdx.y * kRows;
   if (d.rows <= r0 || d.first >= (int64_t)c * d.run) return;  // no work there, or the cut falls between units
-  const int64_t c0 = d.first / d.run, c1 = (d.last - 1) / d.run;
+  const int64_t c0 = div64(d.first, d.run), c1 = div64(d.last - 1, d.run);
   if (c0 + 1 != c) return;  // an earlier cut of the same unit
   const int parts = (int)(c1 - c0) + 1;
   // parts: the end of run c0 (its only segment, or its last), then the beginnings of the others
   const int64_t slot0 = d.first == c0 * d.run ? 2 * c0 : 2 * c0 + 1;
-  float m[kRows], l[kRows], lr[kRows], o[kRows][kPer];
+  auto load = [&](int p, int r, float4& ml, float (&v)[kPer]) {  // lane l: elements kPer l .. kPer l + kPer - 1
+    const int64_t at = (p == 0 ? slot0 : 2 * (c0 + p)) * N + r0 + r;
+    ml = reinterpret_cast<const float4*>(a.part_ml)[at];
+    if constexpr (kPer == 4) {
+      const float4 x = reinterpret_cast<const float4*>(a.part_o + at * D)[lane];
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = reinterpret_cast<const float2*>(a.part_o + at * D)[lane];
+      v[0] = x.x, v[1] = x.y;
+    }
+  };
+  JoinSum<D> sum;
+  if (parts <= 8) {
+    for (int p0 = 0; p0 < parts; p0 += 4) {
+      float4 ml[4];
+      float v[4][kPer];
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    m[r] = kNoMax;
-    l[r] = lr[r] = 0.f;
+      for (int i = 0; i < 4; ++i)
+        if (p0 + i < parts) load(p0 + i, warp, ml[i], v[i]);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) o[r][i] = 0.f;
-  }
-  for (int p = warp; p < parts; p += 8) {
-    const int64_t slot = p == 0 ? slot0 : 2 * (c0 + p);
+      for (int i = 0; i < 4; ++i)
+        if (p0 + i < parts) sum.add(ml[i].x, ml[i].y, ml[i].z, v[i]);
+    }
+  } else {
+    JoinSum<D> row[kRows];
+    for (int p = warp; p < parts; p += 4) {
+      float4 ml[kRows];
+      float v[kRows][kPer];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) load(p, r, ml[r], v[r]);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) row[r].add(ml[r].x, ml[r].y, ml[r].z, v[r]);
+    }
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t row = slot * N + r0 + r;
-      const float4 ml = reinterpret_cast<const float4*>(a.part_ml)[row];
-      const float pm = ml.x;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) so[warp][r][lane * kPer + i] = row[r].o[i];
+      if (lane == 0) {
+        sm[warp][r][0] = row[r].m;
+        sm[warp][r][1] = row[r].l;
+        sm[warp][r][2] = row[r].lr;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
       float v[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = a.part_o[row * D + lane + 32 * i];
-      const float top = fmaxf(m[r], pm), f = ex2(m[r] - top), pf = ex2(pm - top);
-      m[r] = top;
-      l[r] = l[r] * f + ml.y * pf;
-      lr[r] = lr[r] * f + ml.z * pf;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) o[r][i] = o[r][i] * f + v[i] * pf;
+      for (int i = 0; i < kPer; ++i) v[i] = so[w][warp][lane * kPer + i];
+      sum.add(sm[w][warp][0], sm[w][warp][1], sm[w][warp][2], v);
     }
   }
-#pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) so[warp][r][lane + 32 * i] = o[r][i];
-    if (lane == 0) {
-      sm[warp][r] = m[r];
-      sl[warp][r] = l[r];
-      sr[warp][r] = lr[r];
-    }
-  }
-  __syncthreads();
-  const int r = warp;  // one warp a row
-  if (r >= kRows || r0 + r >= d.rows) return;
-  float top = kNoMax, sum = 0.f, rounded = 0.f;
-  for (int w = 0; w < 8; ++w) top = fmaxf(top, sm[w][r]);
-  for (int w = 0; w < 8; ++w) {
-    sum = fmaf(ex2(sm[w][r] - top), sl[w][r], sum);
-    rounded = fmaf(ex2(sm[w][r] - top), sr[w][r], rounded);
-  }
-  const float inv = rounded > 0.f ? 1.f / rounded : 0.f;
-  const int g = a.Hq / a.Hkv, rr = d.row0 + r0 + r, j = rr / g;
+  if (r0 + warp >= d.rows) return;
+  const float inv = sum.lr > 0.f ? 1.f / sum.lr : 0.f;
+  const int g = a.Hq / a.Hkv, rr = d.row0 + r0 + warp, j = rr / g;
   const int64_t orow = (int64_t)(d.q0 + j) * a.Hq + d.hk * g + (rr - j * g);
-  for (int e = lane; e < a.d; e += 32) {
-    float x = 0.f;
-    for (int w = 0; w < 8; ++w) x = fmaf(ex2(sm[w][r] - top), so[w][r][e], x);
-    static_cast<__nv_bfloat16*>(a.out)[orow * a.d + e] = __float2bfloat16_rn(x * inv);
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2) {  // d is even here
+    const int e = lane * kPer + i;
+    if (e < a.d) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.d + e) = pack_bf16(sum.o[i] * inv, sum.o[i + 1] * inv);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[orow] = sum > 0.f ? (top + log2f(sum)) * 0.693147181f : -INFINITY;
+  if (lane == 0 && a.lse != nullptr) a.lse[orow] = sum.l > 0.f ? (sum.m + log2f(sum.l)) * 0.693147181f : -INFINITY;
 }
 
 // ----------------------------------------------------------------------------
@@ -1549,7 +1575,7 @@ static int launch_attend_tc(const TcAttend& t, int grid, cudaStream_t st) {
   // for the whole grid before it reads a part.
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid - 1, N / 4);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

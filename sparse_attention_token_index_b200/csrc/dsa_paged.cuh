@@ -40,22 +40,13 @@ struct RowSeq {
   int pos;   // the row's position, -1 or below: it sees nothing
 };
 
-// Finds the request whose rows hold `row` (offsets ascend; a request without
-// rows is passed over).  Reports a request that breaks the call's rules.
-__device__ __forceinline__ RowSeq find_row(const AttendArgs& a, int row) {
+// Row `row` of request lo, if that request keeps the call's rules; else
+// reports it.
+__device__ __forceinline__ RowSeq row_of(const AttendArgs& a, int lo, int row) {
   RowSeq r;
   r.b = -1;
   r.len = 0;
   r.pos = -1;
-  if (row >= a.q_off[a.B]) return r;  // padding behind the last request
-  int lo = 0, hi = a.B - 1;           // the last b with q_off[b] <= row
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.q_off[mid] <= row)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
   const int q0 = a.q_off[lo], q1 = a.q_off[lo + 1], len = a.lens[lo];
   if (q0 < 0 || row < q0 || row >= q1 || q1 > a.total_q || (a.idx == nullptr && q1 - q0 > a.max_q) || len < 0 ||
       (int64_t)len > (int64_t)a.max_pages * a.page) {
@@ -66,6 +57,26 @@ __device__ __forceinline__ RowSeq find_row(const AttendArgs& a, int row) {
   r.len = len;
   r.pos = len - (q1 - q0) + (row - q0);
   return r;
+}
+
+// Finds the request whose rows hold `row` (offsets ascend; a request without
+// rows is passed over).
+__device__ __forceinline__ RowSeq find_row(const AttendArgs& a, int row) {
+  if (row >= a.q_off[a.B]) return RowSeq{-1, 0, -1};  // padding behind the last request
+  int lo = 0, hi = a.B - 1;                            // the last b with q_off[b] <= row
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.q_off[mid] <= row)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return row_of(a, lo, row);
+}
+
+// a / b (a >= 0, b > 0); the 32-bit division is several times shorter.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Page id of `pos` of request b (0 <= pos < len), -1 if the table names a

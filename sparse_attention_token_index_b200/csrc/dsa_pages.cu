@@ -56,17 +56,29 @@ __device__ __forceinline__ void block_scan2(int64_t (&v)[2], int64_t (&total)[2]
     warp_sum[warp][1] = inc[1];
   }
   __syncthreads();
+  int64_t w[2];  // every warp adds up the warps' sums
+#pragma unroll
+  for (int i = 0; i < 2; ++i) w[i] = lane < warps ? warp_sum[lane][i] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, w[i], o);
+      if (lane >= o) w[i] += u;
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += warp_sum[w][i];
-      all += warp_sum[w][i];
-    }
-    v[i] = inc[i] - v[i] + before;
-    total[i] = all;
+    const int64_t before = __shfl_sync(0xffffffffu, w[i], warp > 0 ? warp - 1 : 0);
+    v[i] = inc[i] - v[i] + (warp > 0 ? before : 0);
+    total[i] = __shfl_sync(0xffffffffu, w[i], 31);
   }
   __syncthreads();
+}
+
+// ceil(n / page): both below 2^31, so their sum is an unsigned 32-bit number.
+__device__ __forceinline__ int pages_of(int n, int page) {
+  return (int)(((unsigned)n + (unsigned)page - 1u) / (unsigned)page);
 }
 
 // New tokens and new pages of request b; false if its lengths break a rule.
@@ -78,7 +90,7 @@ __device__ __forceinline__ bool plan_request(const PlanArgs& a, int b, int64_t (
     return false;
   }
   v[0] = m;
-  v[1] = (n + m + a.page - 1ll) / a.page - (n + a.page - 1ll) / a.page;
+  v[1] = pages_of(n + m, a.page) - pages_of(n, a.page);
   return true;
 }
 
@@ -155,8 +167,7 @@ __device__ __forceinline__ int fresh_page(const PlanArgs& a, int used, int i) {
   return -1;
 }
 
-// Table entries t, t + step, ... and tokens 4 t .. 4 t + 3, 4 (t + step) ...
-// q_off, first [B + 1] and lens [B] (new tokens included): the sums, in
+// Thread t of `step`: table entries t, t + step, ... and its share of the tokens.  q_off, first [B + 1] and lens [B] (new tokens included): the sums, in
 // global or shared memory.
 __device__ __forceinline__ void plan_fill(const PlanArgs& a, const int32_t* q_off, const int32_t* first,
                                           const int32_t* lens, int used, int64_t t, int64_t step) {
@@ -164,58 +175,41 @@ __device__ __forceinline__ void plan_fill(const PlanArgs& a, const int32_t* q_of
   for (int64_t i = t; i < n_fresh; i += step) {
     const int b = bisect(first, a.B, (int)i);
     const int len = lens[b] - (q_off[b + 1] - q_off[b]);
-    const int held = (int)((len + a.page - 1ll) / a.page);
+    const int held = pages_of(len, a.page);
     a.table[(int64_t)b * a.max_pages + held + ((int)i - first[b])] = fresh_page(a, used, (int)i);
   }
-  for (int64_t i0 = t * 4; i0 < a.max_tokens; i0 += step * 4) {
-    int64_t slot[4];
-    int pos[4];
-    int b = -1, next = 0, len = 0, held = 0, q0 = 0, col = -1, id = -1;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t i = i0 + e;
-      slot[e] = -1;
-      pos[e] = -1;
-      if (i >= n_new) continue;
-      if (b < 0 || i >= next) {  // another request
-        if (b < 0) {
+  // A warp takes a run of tokens, one a lane and turn (a wider turn is more
+  // code, and a step this short waits for its instructions); a lane's next
+  // token belongs to the same request or one close behind.
+  const int64_t per = (a.max_tokens + step - 1) / step, begin = (t >> 5) * per * 32;
+  const int64_t end = min((int64_t)a.max_tokens, begin + per * 32);
+  int b = 0, q0 = 0, next = 0, len = 0, held = 0;  // the request, its first token and the one behind its last
+#pragma unroll 1
+  for (int64_t i = begin + (t & 31); i < end; i += 32) {
+    int64_t slot = -1;
+    int pos = -1;
+    if (i < n_new) {
+      if (i >= next) {
+        for (int k = 0; k < 3 && next > 0 && i >= next; ++k) next = q_off[++b + 1];
+        if (i >= next) {
           b = bisect(q_off, a.B, (int)i);
-        } else {
-          do ++b;
-          while (q_off[b + 1] <= i);
+          next = q_off[b + 1];
         }
         q0 = q_off[b];
-        next = q_off[b + 1];
         len = lens[b] - (next - q0);
-        held = (int)((len + a.page - 1ll) / a.page);
-        col = -1;
+        held = pages_of(len, a.page);
       }
-      pos[e] = len + (int)i - q0;
-      const int c = pos[e] / a.page;
-      if (c != col) {  // another page
-        col = c;
-        if (col < held) {  // the last page the request held already
-          id = a.table[(int64_t)b * a.max_pages + col];
-          if ((unsigned)id >= (unsigned)a.n_pages) {
-            report_error(a.status, DSA_ERR_INVALID_ARG, 52);
-            id = -1;
-          }
-        } else {
-          id = fresh_page(a, used, first[b] + col - held);
-        }
-      }
-      if (id >= 0) slot[e] = (int64_t)id * a.page + (pos[e] - col * a.page);
+      pos = len + (int)i - q0;
+      const int col = (int)((unsigned)pos / (unsigned)a.page);
+      // the last page the request held already, or one of this step's
+      const int id = *(col < held ? a.table + (int64_t)b * a.max_pages + col : a.free_pages + used + first[b] + col - held);
+      if ((unsigned)id < (unsigned)a.n_pages)
+        slot = (int64_t)id * a.page + (pos - col * a.page);
+      else
+        report_error(a.status, DSA_ERR_INVALID_ARG, 52);
     }
-    if (i0 + 4 <= a.max_tokens) {  // both arrays start on 16 bytes
-      reinterpret_cast<longlong2*>(a.slots + i0)[0] = make_longlong2(slot[0], slot[1]);
-      reinterpret_cast<longlong2*>(a.slots + i0)[1] = make_longlong2(slot[2], slot[3]);
-      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
-      for (int e = 0; i0 + e < a.max_tokens; ++e) {
-        a.slots[i0 + e] = slot[e];
-        a.positions[i0 + e] = pos[e];
-      }
-    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
   }
 }
 
@@ -278,10 +272,9 @@ __global__ void __launch_bounds__(256) page_plan_fill_kernel(const PlanArgs a) {
 
 int launch_page_plan(const PlanArgs& a, int sms, cudaStream_t st) {
   const NvtxRange nvtx("dsa.page_plan");
-  // four tokens a thread; a step hands out no more pages than it adds tokens
-  const int64_t items = ((int64_t)a.max_tokens + 3) / 4;
+  const int64_t items = a.max_tokens;  // a step hands out no more pages than it adds tokens
   if (a.B <= kOneRequests && a.lens_out != a.lens && a.used_out != a.used) {
-    // 4 us for 8 requests; for 1024 with a million tokens 9 us in 2 blocks a multiprocessor
+    // 4 us for 8 requests; 12 us for 1024 with a million tokens in 2 blocks a multiprocessor (1: 14, 4: 16)
     const int64_t blocks = (items + kOneThreads - 1) / kOneThreads, most = (int64_t)sms * 2;
     page_plan_kernel<<<(int)(blocks < 1 ? 1 : (blocks < most ? blocks : most)), kOneThreads, 0, st>>>(a);
   } else {
