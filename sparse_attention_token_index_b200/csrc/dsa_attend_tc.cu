@@ -42,8 +42,9 @@
 // which waits for A's bytes from shared memory and takes no longer for it up
 // to 64 columns.  With more rows that costs a quarter of the time (32 caches of
 // 131072 tokens, 128 rows each: 473 us for 366), and the weights are rounded
-// once; the output is divided by the sum of the rounded weights, which leaves
-// rows of few tokens exact.  (e4m3 weights carry V's scales and are always
+// once.  A row of one token stays exact all the same: with rows on the lanes
+// its reference is its score; with 64 rows the output is divided by the sum of
+// the rounded weights.  (e4m3 weights carry V's scales and are always
 // split.)  The log-sum-exp comes from the fp32 sum of the weights themselves.
 //
 // With tokens on the lanes a thread sees many rows, and their
@@ -457,7 +458,7 @@ struct AttendSmem {
   uint64_t s_full[2], p_full[2], p_empty[2];
   uint64_t o_full[2], o_free[2], tok_full[kTok], tok_empty[kTok], drain;
   float red[2][4][N / 2 > 32 ? 32 : N / 2];
-  float sum[2][2][C::kRows ? N : 1], red2[2][4][N == 64 && C::kSplit == false ? 32 : 1];
+  float sum[2][C::kRows ? N : 1], red2[2][4][N == 64 && C::kSplit == false ? 32 : 1];
   alignas(16) float nref[N];
   float rowmax[N], cref[2];
   int common[2];
@@ -893,8 +894,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
     Seg s;
     const int wg = warp >> 2, wq = warp & 3, tid = threadIdx.x & 127;
-    constexpr int kGroup = C::kRows ? 256 : 128;
-    const int bar = C::kRows ? 1 : 1 + wg;
+    // who shares references: the two warps of 32 rows, or the four of half the rows
+    constexpr int kGroup = C::kRows ? 64 : 128;
+    const int bar = C::kRows ? 1 + wq : 1 + wg;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
     const float c2 = a.scale * 1.44269504f;  // scores in powers of two
     int n = 0, seg = 0;
@@ -954,7 +956,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const int rr = s.row0 + r, jq = rr / g;
         const int orow = r < s.rows ? (s.q0 + jq) * a.Hq + s.hk * g + (rr - jq * g) : -1;
         const int lim = kSel ? 0x7fffffff : s.lim0 + jq;
-        float nref = -kNoMax, l = 0.f, lr = 0.f;  // sums of the weights, and of their bf16
+        float nref = -kNoMax, l = 0.f;
         for (int j = 0; j < s.tiles; ++j, ++n) {
           const int tile = s.tile0 + j, tk = n % kTok;
           if constexpr (kSel || kFp8) ok = ok && mbar_wait(&S.tok_full[tk], (n / kTok) & 1, abort_flag, a.status, 94, budget);
@@ -1021,7 +1023,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             const float fac = ex2(-nref - m);
             nref = -m;
             l *= fac;
-            lr *= fac;
             if (j > 0) {  // the output tile holds the tiles before: wait for the last of them, then scale
               ok = ok && mbar_wait(&S.p_empty[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag, a.status, 91, budget);
               ok = __all_sync(0xffffffffu, ok);
@@ -1045,7 +1046,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           float2 l2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < 64; i += 4) {
-            const float2 u = make_float2(ex2(x[i]), ex2(x[i + 1])), v = make_float2(ex2(x[i + 2]), ex2(x[i + 3]));
+            const float2 u = make_float2(ex2(x[i]), ex2(x[i + 1]));
+            const float2 v = make_float2(ex2(x[i + 2]), ex2(x[i + 3]));
             l2 = add2(l2, add2(u, v));
             float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
             if constexpr (kFp8) vs = *reinterpret_cast<const float4*>(&S.vsc[tk][c0 + i]);
@@ -1062,23 +1064,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             tc_fence_after();
           }
           const uint32_t pcol = tmem_base + lanes + (uint32_t)(C::kPCol + (C::kPBufs == 2 ? (n & 1) * 64 : 0) + wg * 32);
-          float2 r2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i0 = 0; i0 < 64; i0 += 16) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if constexpr (C::kSplit) {
+              if constexpr (C::kSplit)
                 split_bf16(x[i0 + 2 * i], x[i0 + 2 * i + 1], hi[i], lo[i]);
-              } else {
+              else
                 hi[i] = pack_bf16(x[i0 + 2 * i], x[i0 + 2 * i + 1]);
-                r2 = add2(r2, unpack_bf16(hi[i]));
-              }
             }
             tmem_st8(pcol + (i0 >> 1), hi);
             if constexpr (C::kSplit) tmem_st8(pcol + 64 + (i0 >> 1), lo);
           }
-          lr += r2.x + r2.y;
           l += l2.x + l2.y;
           tmem_st_wait();
           tc_fence_before();
@@ -1094,21 +1092,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           ok = false;
           break;
         }
-        S.sum[wg][0][r] = l;
-        S.sum[wg][1][r] = lr;
+        S.sum[wg][r] = l;
         named_bar(bar, kGroup);
-        const float sum = S.sum[0][0][r] + S.sum[1][0][r];
-        const float rounded = C::kSplit ? sum : S.sum[0][1][r] + S.sum[1][1][r];
+        const float sum = S.sum[0][r] + S.sum[1][r];
         pend = true;
         pend_whole = s.tiles == s.unit_tiles;
         pend_part = 2 * (int64_t)blockIdx.x + (first_seg ? 0 : 1);
         pend_par = seg % C::kOBufs;
         pend_phase = (seg / C::kOBufs) & 1;
         pend_row = orow;
-        pend_inv = rounded > 0.f ? 1.f / rounded : 0.f;
+        pend_inv = sum > 0.f ? 1.f / sum : 0.f;
         if (wg == 0) {
           if (!pend_whole) {
-            reinterpret_cast<float4*>(a.part_ml)[pend_part * N + r] = make_float4(-nref, sum, rounded, 0.f);
+            reinterpret_cast<float4*>(a.part_ml)[pend_part * N + r] = make_float4(-nref, sum, sum, 0.f);
           } else if (a.lse != nullptr && orow >= 0) {
             a.lse[orow] = sum > 0.f ? (log2f(sum) - nref) * 0.693147181f : -INFINITY;
           }
