@@ -8,8 +8,12 @@
 //     O^T [d x N rows]         += V^T P^T     (A = V^T tile, B = P)
 // with the tokens, never the few query rows, on the 128-lane side of the
 // product, so no lane is spent on padding: a softmax thread owns one token
-// and N/2 of its rows.  Decoding reads each K and V row once for N rows, 2 N
-// flops a byte, and at N <= 128 memory is the bound.
+// and N/2 of its rows.  Beyond 64 rows (N = 128) the query rows fill the lanes
+// themselves, S = Q K^T and O += P V: a thread owns half a row, whose statistics
+// stay in its registers, and the weights are the A operand in tensor memory
+// (128 rows over 32 caches of 131072 tokens: 385 us, 901 with tokens on the
+// lanes).  Decoding reads each K and V row once for N rows, 2 N flops a byte,
+// and at N <= 128 memory is the bound.
 //
 // One persistent CTA per SM:
 //   * three lookup warps turn positions into cache rows (page table, or list
@@ -25,8 +29,8 @@
 //     and are written as bf16 (exact);
 //   * the MMA warp issues S(t+1) before O(t), so that the tensor pipe has
 //     work while the softmax of a tile runs;
-//   * eight softmax warps: four cover the 128 tokens for the first N/2 rows,
-//     four for the rest.
+//   * eight softmax warps: four cover the 128 lanes for the first half of the
+//     columns, four for the rest.
 //
 // The reference m is not the running maximum but one that no score has
 // passed by more than 2^16: as long as that holds no sum needs rescaling, and
@@ -47,10 +51,10 @@
 // the rounded weights.  (e4m3 weights carry V's scales and are always
 // split.)  The log-sum-exp comes from the fp32 sum of the weights themselves.
 //
-// With tokens on the lanes a thread sees many rows, and their
-// references come from shared memory, where the copies queue; so the rows
-// share one, in a register, while no row's maximum is below it by more than
-// 2^64 (fp32 and bf16 hold 2^-126), and have their own beyond that.
+// With tokens on the lanes a thread sees many rows, and their references come
+// from shared memory, where the copies queue; so the rows share one, in a
+// register, while no row's maximum is below it by more than 2^64 (fp32 and
+// bf16 hold 2^-126), and have their own beyond that.
 //
 // The work (all tiles of all requests and key heads, end to end) is cut into
 // equal runs, one per CTA, wherever the cuts fall: ragged batches and single
@@ -66,9 +70,10 @@ namespace dsa {
 constexpr int kTile = 128;           // tokens a tile
 constexpr int kSoftWarps = 8, kLookWarps = 3, kCopyWarps = 16;
 constexpr int kWarps = kSoftWarps + 1 + kLookWarps + kCopyWarps;
+constexpr int kLaunchRegs = 72;      // registers a thread at launch: 65536 over 28 warps
 constexpr float kNoMax = -1.7e38f;   // reference of a row that has seen no token
 constexpr float kSlack = 16.f;       // log2 of the largest weight
-constexpr float kSpread = 64.f;      // log2 of the largest weight of a row that shares its reference, at least 2^-this
+constexpr float kSpread = 64.f;      // how far (log2) a shared reference may lie above a row's own maximum
 
 struct TcAttend {
   AttendArgs a;
@@ -431,9 +436,8 @@ struct Cfg {
   static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   // Registers a thread: launched with 72 (28 warps), of which the copy warps
   // give some up, so that the softmax warps hold a row's or token's scores.
-  // 256 x kSoftRegs + 128 x kMidRegs + 512 x kCopyRegs <= 896 x 72.
   static constexpr int kSoftRegs = kFp8 ? 128 : 144, kMidRegs = 56, kCopyRegs = kFp8 ? 48 : 40;
-  static_assert(256 * kSoftRegs + 128 * kMidRegs + 512 * kCopyRegs <= kWarps * 32 * 72, "the registers of the launch");
+  static_assert(256 * kSoftRegs + 128 * kMidRegs + 512 * kCopyRegs <= kWarps * 32 * kLaunchRegs, "the registers of the launch");
   // Tensor memory: two score tiles; with rows on the lanes the weights, two
   // tiles or one and its rests (64 columns each); two output tiles, one where
   // no more fit (tokens on the lanes: the columns of the rests are added when
@@ -1559,6 +1563,10 @@ static int launch_attend_tc(const TcAttend& t, int grid, cudaStream_t st) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return DSA_ERR_CUDA;
   const uint64_t bit = uint64_t(1) << dev;
   if (!(configured.load(std::memory_order_acquire) & bit)) {
+    // the roles' registers add up to what the launch brings; with fewer their shares would never come
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, attend_tc_kernel<N, D, kFp8, kSel>) != cudaSuccess) return DSA_ERR_CUDA;
+    if (attr.numRegs != kLaunchRegs) return DSA_ERR_INTERNAL;
     if (cudaFuncSetAttribute(attend_tc_kernel<N, D, kFp8, kSel>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)kSmem) != cudaSuccess)
       return DSA_ERR_CUDA;
