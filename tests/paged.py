@@ -80,6 +80,11 @@ class Step:
             self.idx = torch.from_numpy(idx).to(DEV)
         self.max_q = max(news + [1])
 
+    @property
+    def shared(self):
+        """Query rows that read the same tokens, at most."""
+        return self.Hq // self.Hkv * (self.max_q if self.idx is None else 1)
+
     def args(self):
         return (self.Q, self.K, self.V, self.table, self.lens_t, self.q_off)
 
@@ -100,7 +105,11 @@ def check(step, out, lse, scale=None, what=""):
     exponential.  Sums over n tokens add n 2^-23.  The tensor-core kernel
     rounds each weight to bf16 (half a step: 2^-8), and bf16 outputs round
     once more.  All of it acts on sum p |v|; the log-sum-exp sees the scores'
-    error and the sum's only."""
+    error and the sum's only.  Where 33 to 64 bf16 query rows share their
+    tokens the output is N / D with N = sum p^ v, D = sum p^ of the rounded
+    weights p^ = p (1 + e), |e| <= 2^-8: N / D - ref = (N - ref - ref (D - 1)) / D,
+    so |N / D - ref| <= (2^-8 sum p |v| + 2^-8 |ref|) / (1 - 2^-8): the
+    denominator's rounding adds 2^-8 |ref|, and 1 / D the factor 1 + 2^-7."""
     ref, rlse, mag, top, count = step.oracle(scale)
     live = ~np.isnan(rlse[:, 0])
     o, l = f64(out)[live], lse.double().cpu().numpy()[live]
@@ -110,6 +119,8 @@ def check(step, out, lse, scale=None, what=""):
     half = 2.0 ** -24 if step.kv == "fp32" else 2.0 ** -8
     weights = 0.0 if step.kv == "fp32" else 2.0 ** -8
     tol = half * np.abs(ref) + (dw[..., None] * (1 + half) + weights * (1 + half)) * mag
+    if step.kv == "bf16" and 32 < getattr(step, "shared", 0) <= 64:
+        tol = half * np.abs(ref) + (dw[..., None] * (1 + half) * mag + weights * (1 + half) * (mag + np.abs(ref))) * (1 + 2.0 ** -7)
     bad = ~(np.abs(o - ref) <= tol)
     assert not bad.any(), (what, int(bad.sum()), float(np.nanmax(np.abs(o - ref)[bad])), np.argwhere(bad)[:4].tolist())
     none = count[:, 0] == 0

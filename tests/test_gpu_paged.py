@@ -1,5 +1,10 @@
 """Paged-cache calls on the GPU against the float64 oracle: page plan, cache
 write, attention over all cached tokens and over chosen positions."""
+import os
+import random
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -616,3 +621,43 @@ def test_the_extension_leaves_what_it_does_not_take():
         dsa.dsa_attend_paged(*step.args(), 0, workspace=ws)
     with pytest.raises(dsa.DsaError):
         dsa.dsa_page_plan(step.lens_t, step.lens_t, step.table, step.lens_t, step.lens_t[:1], 0, 4, 8, workspace=ws)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("seed", range(6))
+def test_attend_random_shapes(kv, seed):
+    """Group sizes, head sizes, pages and lengths as they fall, short rows and padded batches among them."""
+    rng = random.Random(seed * 2 + (kv == "e4m3"))
+    for _ in range(12):
+        Hkv, g = rng.choice([(1, 1), (2, 3), (1, 5), (3, 7), (8, 8), (1, 17), (2, 33), (1, 48), (1, 64), (1, 65), (1, 100)])
+        d = rng.choice([8, 48, 64, 80, 112, 128]) if kv == "bf16" else rng.choice([16, 64, 80, 128])
+        lens = [rng.randint(0, rng.choice([3, 130, 600])) for _ in range(rng.randint(1, 8))]
+        news = [rng.randint(0, rng.choice([1, 2, 4])) for _ in lens]
+        k = rng.choice([None, 1, 63, 129, 300])
+        step = Step(lens, news, Hkv * g, Hkv, d, kv, page=rng.choice([1, 5, 16, 64, 300]), pad=rng.randint(1, 3),
+                    joint=rng.random() < 0.3, k=k, seed=rng.randint(0, 1 << 30), spread=rng.choice([0.1, 1.5, 8.0]))
+        _both(step, what=(Hkv, g, d, lens, news, k))
+
+
+def test_first_calls_in_a_capture():
+    # a process whose first attention calls are captured: nothing of theirs may need the host
+    code = """
+import torch
+import sparse_attention_token_index_b200 as dsa
+from tests.paged import Step, check
+step = Step([300, 7, 129], [2, 1, 3], 8, 2, 64, "bf16", k=50)
+ws = torch.zeros(32 << 20, dtype=torch.uint8, device="cuda")
+side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+    a = dsa.dsa_attend_paged(*step.args(), step.max_q, return_lse=True, workspace=ws)
+    b = dsa.dsa_attend_selected(*step.args(), step.idx, return_lse=True, workspace=ws)
+g.replay()
+torch.cuda.synchronize()
+check(step, *b)
+step.idx = None
+check(step, *a)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
