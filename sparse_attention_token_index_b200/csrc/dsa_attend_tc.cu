@@ -1330,7 +1330,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
               for (int i0 = 0; i0 < kC; i0 += 8) {
 #pragma unroll
-                for (int rest = 0; rest < 2; ++rest) {
+                for (int rest = 0; rest < C::kPCols / N; ++rest) {  // the rests' columns too, where there are any
                   float v[8];
                   uint32_t w[8];
                   tmem_ld<8>(o + rest * N + i0, v);
