@@ -48,7 +48,8 @@
 // 131072 tokens, 128 rows each: 473 us for 366), and the weights are rounded
 // once.  A row of one token stays exact all the same: with rows on the lanes
 // its reference is its score; with 64 rows the output is divided by the sum of
-// the rounded weights.  (e4m3 weights carry V's scales and are always
+// the rounded weights, and references are whole numbers there, so that weights
+// rounded against an old one stay those that the product took.  (e4m3 weights carry V's scales and are always
 // split.)  The log-sum-exp comes from the fp32 sum of the weights themselves.
 //
 // With tokens on the lanes a thread sees many rows, and their references come
@@ -1297,7 +1298,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
               float tile_max = S.red[wg][0][lane % kC];
 #pragma unroll
               for (int w = 1; w < 4; ++w) tile_max = fmaxf(tile_max, S.red[wg][w][lane % kC]);
-              const float row_max = fmaxf(S.rowmax[r], tile_max), own = fmaxf(old, tile_max);
+              const float row_max = fmaxf(S.rowmax[r], tile_max);
+              // weights that are rounded once: whole numbers, so that a scaled sum of rounded weights is one of scaled ones
+              const float own = fmaxf(old, C::kSplit ? tile_max : ceilf(tile_max));
               float hi = own, lo = row_max <= kNoMax ? INFINITY : row_max;
 #pragma unroll
               for (int w = 16; w > 0; w >>= 1) {
@@ -1312,7 +1315,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
                 S.rowmax[r] = row_max;
                 S.nref[r] = -ref;
                 // a jump that the weights just summed may not have held: 2^-96 of what stood before is nothing beside them
-                S.fac[r] = ref - old > 96.f ? 0.f : ex2(old - ref);
+                S.fac[r] = ref - old > 96.f ? 0.f : C::kSplit ? ex2(old - ref) : __uint_as_float((uint32_t)(127 - (int)(ref - old)) << 23);
               }
               if (lane == 0) {
                 S.common[wg] = one;
@@ -1345,6 +1348,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             scores();
 #pragma unroll
             for (int i = 0; i < kC; ++i) x[i] = ex2(x[i]);
+            if (!C::kSplit && j > 0) {
+              // what the product takes must be what the sums hold: the bf16 that the first pass left, scaled (exact)
+#pragma unroll
+              for (int i = 0; i < kC; i += 8) {
+                const uint4 w = *reinterpret_cast<const uint4*>(prow + (((p_unit + (i >> 3)) ^ p_sw) << 4));
+                const uint32_t old[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 o = unpack_bf16(old[e]);
+                  const float f0 = S.fac[c0 + i + 2 * e], f1 = S.fac[c0 + i + 2 * e + 1];
+                  x[i + 2 * e] = f0 > 0.f ? o.x * f0 : x[i + 2 * e];
+                  x[i + 2 * e + 1] = f1 > 0.f ? o.y * f1 : x[i + 2 * e + 1];
+                }
+              }
+            }
             put_weights([&](float2& u, int c, float2 w) {  // the sums hold this tile already
               const float f0 = S.fac[c0 + c], f1 = S.fac[c0 + c + 1];
               u.x = f0 > 0.f ? u.x * f0 : w.x;

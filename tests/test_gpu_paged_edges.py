@@ -58,3 +58,30 @@ def test_a_moving_reference_leaves_the_other_outputs(Hq, m, k):
         step.idx.copy_(i32(quiet + loud)[None].expand_as(step.idx))
     loud_tokens(step, (lambda p: p >= 128) if k is None else (lambda p: p % 2 == 1), [20.0, 24.0, 17.0])
     check(step, *run(step))
+
+
+@pytest.mark.parametrize("k", [None, 900])
+@pytest.mark.parametrize("kv,Hq,Hkv,m,d", [("bf16", 64, 1, 1, 128), ("bf16", 40, 1, 1, 64), ("bf16", 33, 1, 1, 128),
+                                           ("bf16", 6, 1, 8, 64), ("bf16", 8, 1, 1, 128), ("bf16", 32, 1, 1, 64),
+                                           ("e4m3", 64, 1, 1, 128), ("e4m3", 128, 1, 1, 128), ("e4m3", 8, 1, 1, 64),
+                                           ("fp32", 8, 2, 2, 64), ("bf16", 8, 2, 2, 256)])
+def test_values_all_alike_come_out_as_they_are(kv, Hq, Hkv, m, d, k):
+    """The weights of a row sum to one in the numbers that the products saw, however its references moved: where every
+    value is v0 (exact in bf16) the output is v0.  Sums of n <= 1000 terms are off by n 2^-23 < 2^-13 relative, two-part
+    weights by 2^-16, both far below half a bf16 step (2^-9 at the least), so the rounding gives v0 itself; fp32 outputs
+    are within 2^-13."""
+    step = Step([700, 1000, 140], [m] * 3, Hq, Hkv, d, kv, page=16, seed=d + Hq, k=k)
+    v0 = (1.0 + torch.arange(d, device=DEV) / 8).to(torch.bfloat16) if kv != "e4m3" else torch.ones(d, device=DEV)
+    if kv == "e4m3":
+        step.V.copy_(torch.where(step.V.float().isnan(), step.V.float(), v0).to(step.V.dtype))
+        step.scales[1].copy_(torch.where(step.scales[1].isnan(), step.scales[1], 1.5))
+        v0 = v0 * 1.5
+    else:
+        step.V.copy_(torch.where(step.V.float().isnan(), step.V.float(), v0.float()).to(step.V.dtype))
+        # jumps below and above the slack of a reference, others beyond what old weights survive
+        loud_tokens(step, lambda p: p % 131 == 130 or p >= 650, [9.3, 14.7, 23.1, 3.9, 47.3, 90.1])
+    out, _ = run(step)
+    if kv == "fp32":
+        assert float((out / v0.float() - 1).abs().max()) <= 2.0 ** -13
+    else:
+        assert torch.equal(out.float(), v0.float().expand_as(out))
