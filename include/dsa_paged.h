@@ -17,9 +17,10 @@
  * an element is e4m3(byte) * scale[page, offset, head].
  *
  * Conventions are those of dsa_index.h: device pointers on the current
- * device, 16-byte aligned (pages: aligned to their element, though pages on
- * 16 bytes are written and read faster), contiguous unless a stride is named;
- * outputs overlap inputs only where a call says so; the caller
+ * device, contiguous unless a stride is named; outputs overlap inputs only
+ * where a call says so.  Q, k, v, out and the workspace are 16-byte aligned,
+ * all else to its element (pages on 16 bytes are written and read faster);
+ * other pointers are refused (DSA_ERR_INVALID_ARG).  The caller
  * owns every buffer; the first bytes of the workspace hold the status word
  * (zero its first 8 bytes before its first use, read it with
  * dsa_check_status); calls are asynchronous on `stream`, allocate nothing and

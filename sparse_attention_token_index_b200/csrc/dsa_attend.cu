@@ -281,7 +281,11 @@ using namespace dsa;
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether every pointer is a multiple of n bytes (null ones are).
+template <typename... P>
+bool aligned(uintptr_t n, const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (n - 1)) == 0;
+}
 
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -367,8 +371,8 @@ int attend(AttendArgs& a, const float* softmax_scale, int q_dtype, int kv_dtype,
   const bool scaled = kv_dtype == DSA_DTYPE_FP8_E4M3;
   if (scaled != (a.K_scale != nullptr) || scaled != (a.V_scale != nullptr)) return DSA_ERR_INVALID_ARG;
   const uintptr_t elt = kv_dtype == DSA_DTYPE_FP32 ? 4 : (kv_dtype == DSA_DTYPE_BF16 ? 2 : 1);
-  if (!aligned16(a.Q) || !aligned16(a.out) || !aligned16(workspace) || reinterpret_cast<uintptr_t>(a.K) % elt ||
-      reinterpret_cast<uintptr_t>(a.V) % elt)
+  if (!aligned(16, a.Q, a.out, workspace) || !aligned(elt, a.K, a.V) ||
+      !aligned(4, a.table, a.lens, a.q_off, a.idx, a.K_scale, a.V_scale, a.lse))
     return DSA_ERR_INVALID_ARG;
   int sms = 0;
   if ((r = current_device(nullptr, &sms)) != DSA_OK) return r;

@@ -518,7 +518,11 @@ using namespace dsa;
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether every pointer is a multiple of n bytes (null ones are).
+template <typename... P>
+bool aligned(uintptr_t n, const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & (n - 1)) == 0;
+}
 
 size_t plan_bytes(int B) { return sizeof(WsHeader) + 256 + (((size_t)B + 1) * 4 + 255) / 256 * 256; }
 
@@ -543,6 +547,9 @@ int dsa_page_plan(const int32_t* lens, const int32_t* new_lens, const int32_t* f
   if (!lens || !new_lens || !used || !block_table || !q_offsets || !lens_out || !used_out || !workspace)
     return DSA_ERR_INVALID_ARG;
   if ((n_free > 0 && !free_pages) || (max_tokens > 0 && (!slots || !positions))) return DSA_ERR_INVALID_ARG;
+  if (!aligned(16, workspace) || !aligned(8, slots) ||
+      !aligned(4, lens, new_lens, free_pages, used, block_table, q_offsets, positions, lens_out, used_out))
+    return DSA_ERR_INVALID_ARG;
   if (workspace_bytes < plan_bytes(B)) return DSA_ERR_WORKSPACE;
   int sms = 0;
   const int r = current_device(nullptr, &sms);
@@ -584,7 +591,7 @@ int dsa_page_append(const void* k, const void* v, const int64_t* slots, int T, i
   const bool scaled = kv_dtype == DSA_DTYPE_FP8_E4M3;
   if (scaled != (K_scale != nullptr) || (scaled && V != nullptr) != (V_scale != nullptr)) return DSA_ERR_INVALID_ARG;
   const uintptr_t elt = kv_dtype == DSA_DTYPE_FP32 ? 4 : (kv_dtype == DSA_DTYPE_BF16 ? 2 : 1);
-  if (!aligned16(k) || !aligned16(v) || reinterpret_cast<uintptr_t>(K) % elt || reinterpret_cast<uintptr_t>(V) % elt)
+  if (!aligned(16, k, v, workspace) || !aligned(elt, K, V) || !aligned(8, slots) || !aligned(4, K_scale, V_scale))
     return DSA_ERR_INVALID_ARG;
   if (workspace_bytes < sizeof(WsHeader)) return DSA_ERR_WORKSPACE;
   int sms = 0;

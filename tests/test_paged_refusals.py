@@ -1,0 +1,52 @@
+"""Calls of the paged cache that the host refuses or answers without a device:
+what would fault, be cut short or be answered wrongly further on (CPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_attention_token_index_b200 as dsa
+from test_paged_api import BF16, E4M3, OK, _attend, _plan
+
+
+@pytest.fixture(scope="module")
+def L():
+    return dsa.lib()
+
+
+def at(offset):
+    return ctypes.c_void_p(4096 + offset)
+
+
+# ---------------------------------------------------------------------------
+# addresses
+# ---------------------------------------------------------------------------
+def _append(L, **kw):
+    a = dict(k=OK, v=OK, slots=OK, T=4, Hkv=8, d=128, src=BF16, kv=BF16, K=OK, V=OK, ks=None, vs=None, n_pages=4,
+             page=16, stride=16 * 8 * 128, ws=OK, wb=256)
+    a.update(kw)
+    return L.dsa_page_append(a["k"], a["v"], a["slots"], a["T"], a["Hkv"], a["d"], a["src"], a["kv"], a["K"], a["V"],
+                             a["ks"], a["vs"], a["n_pages"], a["page"], a["stride"], a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("name,offset", [("ws", 1), ("ws", 8), ("slots", 4), ("lens", 2), ("new", 1), ("free", 2), ("used", 2),
+                                         ("table", 1), ("q", 2), ("pos", 2), ("lo", 2), ("uo", 3)])
+def test_plan_refuses_addresses_off_their_element(L, name, offset):
+    assert _plan(L, **{name: at(offset)}) == -1
+
+
+@pytest.mark.parametrize("name,offset", [("ws", 1), ("ws", 8), ("slots", 4), ("k", 8), ("v", 2), ("K", 1), ("V", 1), ("ks", 2),
+                                         ("vs", 1)])
+def test_append_refuses_addresses_off_their_element(L, name, offset):
+    scaled = dict(kv=E4M3, ks=OK, vs=OK) if name in ("ks", "vs") else {}
+    assert _append(L, **{**scaled, name: at(offset)}) == -1
+
+
+@pytest.mark.parametrize("selected", [False, True])
+@pytest.mark.parametrize("name,offset", [("ws", 1), ("ws", 8), ("table", 2), ("lens", 1), ("q", 2), ("idx", 2), ("lse", 2), ("ks", 2),
+                                         ("vs", 1), ("Q", 8), ("out", 8), ("K", 1)])
+def test_attention_refuses_addresses_off_their_element(L, selected, name, offset):
+    if name == "idx" and not selected:
+        return
+    scaled = dict(kv=E4M3, ks=OK, vs=OK) if name in ("ks", "vs") else {}
+    assert _attend(L, selected, **{**scaled, name: at(offset)}) == -1
