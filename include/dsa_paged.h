@@ -59,7 +59,8 @@ extern "C" {
  * it was and answers with no tokens: q_offsets 0, slots and positions -1,
  * lens_out = lens, used_out = used.  A page id outside 0 .. n_pages - 1 is
  * recorded as DSA_ERR_INVALID_ARG; the slots in it are -1.
- * B = 0 is an empty call.  B <= 2^20, max_pages * page < 2^31.
+ * B = 0 is an empty call: nothing is launched and every output stays as it
+ * was.  B <= 2^20, max_pages * page < 2^31.
  * ---------------------------------------------------------------------- */
 int dsa_page_plan_workspace_size(int B, int max_tokens, size_t* bytes);
 int dsa_page_plan(const int32_t* lens, const int32_t* new_lens, const int32_t* free_pages, int n_free,

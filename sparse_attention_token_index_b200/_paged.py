@@ -206,8 +206,6 @@ def dsa_page_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
             out = (empty(B + 1, dtype=i32, device=dev), empty(max_tokens, dtype=i64, device=dev),
                    empty(max_tokens, dtype=i32, device=dev), empty(B, dtype=i32, device=dev),
                    empty(1, dtype=i32, device=dev))
-            if B == 0:  # nothing is launched: the answer of a step without requests
-                out[0].zero_(), out[1].fill_(-1), out[2].fill_(-1), out[4].copy_(used)
         else:
             for t, what, dtype, n in zip(out, ("q_offsets", "slots", "positions", "lens_out", "used_out"),
                                          (i32, i64, i32, i32, i32), (B + 1, max_tokens, max_tokens, B, 1)):
@@ -220,6 +218,8 @@ def dsa_page_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
                                 ws.data_ptr(), size, st)
         if r:
             _check(r, "dsa_page_plan")
+        if B == 0:  # nothing is launched: the answer of a step without requests
+            out[0].zero_(), out[1].fill_(-1), out[2].fill_(-1), out[4].copy_(used)
         if check:
             _check(lib().dsa_check_status(ws.data_ptr(), st), "device status")
     return out

@@ -1,5 +1,5 @@
 """Paged-cache calls on the GPU at their edges: references that move while
-other outputs wait."""
+other outputs wait, empty steps."""
 import pytest
 import torch
 
@@ -85,3 +85,23 @@ def test_values_all_alike_come_out_as_they_are(kv, Hq, Hkv, m, d, k):
         assert float((out / v0.float() - 1).abs().max()) <= 2.0 ** -13
     else:
         assert torch.equal(out.float(), v0.float().expand_as(out))
+
+
+# ---------------------------------------------------------------------------
+# empty steps
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_of_no_requests_into_prepared_outputs(in_place):
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    used = i32([3])
+    out = (i32([9]), torch.full((5,), 11, dtype=torch.int64, device=DEV), i32([4] * 5), none.clone(),
+           used if in_place else i32([8]))
+    for kw in ({}, {"workspace": torch.zeros(4096, dtype=torch.uint8, device=DEV)}, {"stream": torch.cuda.Stream()}):
+        for t in out[:3]:
+            t.fill_(9)
+        torch.cuda.synchronize()
+        got = dsa.dsa_page_plan(none, none, torch.empty((0, 4), dtype=torch.int32, device=DEV), i32([1, 2, 3, 4]), used, 16, 4, 5,
+                                out=out, **kw)
+        torch.cuda.synchronize()
+        assert got is out
+        assert out[0].tolist() == [0] and out[1].tolist() == [-1] * 5 and out[2].tolist() == [-1] * 5 and out[4].tolist() == [3]
