@@ -101,8 +101,8 @@ int dsa_page_append(const void* k, const void* v, const int64_t* slots, int T, i
  *   skipped, a page id outside the pool hides its tokens, and either records
  *   DSA_ERR_INVALID_ARG (the outputs of such a call are unspecified).
  *   Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 128, d <= 256,
- *   1 <= max_q <= 65536.  fp32 queries take fp32 pages, bf16 queries bf16 or
- *   e4m3 pages.
+ *   1 <= max_q <= 65536, max_pages * page <= 2^31 - 1024.  fp32 queries
+ *   take fp32 pages, bf16 queries bf16 or e4m3 pages.
  * Sums and softmax statistics are fp32.
  * ---------------------------------------------------------------------- */
 int dsa_attend_paged_workspace_size(int B, int total_q, int max_q, int Hq, int Hkv, int d, int q_dtype,

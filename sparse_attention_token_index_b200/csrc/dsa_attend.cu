@@ -287,6 +287,9 @@ bool aligned(uintptr_t n, const P*... p) {
   return ((reinterpret_cast<uintptr_t>(p) | ...) & (n - 1)) == 0;
 }
 
+// Positions of a request that its table may span.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1024;
+
 size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // A (row, head) has a warp to itself when that makes 16 warps a
@@ -363,7 +366,8 @@ int attend(AttendArgs& a, const float* softmax_scale, int q_dtype, int kv_dtype,
   if (r != DSA_OK) return r;
   if (a.n_pages < 1 || a.page < 1 || a.max_pages < 1 || a.page_stride < (int64_t)a.page * a.Hkv * a.d)
     return DSA_ERR_INVALID_ARG;
-  if ((int64_t)a.max_pages * a.page >= ((int64_t)1 << 31)) return DSA_ERR_UNSUPPORTED;
+  // the kernels round lengths up to tiles and step past them by a block's keys in 32 bits
+  if ((int64_t)a.max_pages * a.page > kMaxTokens) return DSA_ERR_UNSUPPORTED;
   a.scale = softmax_scale != nullptr ? *softmax_scale : 1.f / std::sqrt((float)a.d);
   if (!std::isfinite(a.scale)) return DSA_ERR_INVALID_ARG;
   if (a.B == 0 || a.total_q == 0) return DSA_OK;

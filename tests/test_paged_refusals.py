@@ -50,3 +50,17 @@ def test_attention_refuses_addresses_off_their_element(L, selected, name, offset
         return
     scaled = dict(kv=E4M3, ks=OK, vs=OK) if name in ("ks", "vs") else {}
     assert _attend(L, selected, **{**scaled, name: at(offset)}) == -1
+
+
+# ---------------------------------------------------------------------------
+# sizes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("selected", [False, True])
+def test_attention_refuses_tables_whose_last_tiles_pass_31_bits(L, selected):
+    # a length within a tile of 2^31 overflows where it is rounded up to tiles, or stepped over
+    for page, width in (((1 << 31) - 1, 1), (1, (1 << 31) - 8), (1 << 10, 1 << 21), ((1 << 31) - 1023, 1)):
+        kw = dict(page=page, max_pages=width, Hq=1, Hkv=1, d=8, stride=page * 8)
+        assert _attend(L, selected, **kw) == -2, (page, width)
+    # the largest that is taken goes on to the next check
+    assert _attend(L, selected, page=(1 << 31) - 1024, max_pages=1, Hq=1, Hkv=1, d=8, stride=((1 << 31) - 1024) * 8, Q=None) == -1
+    assert _attend(L, selected, page=1 << 20, max_pages=(1 << 11) - 1, Hq=1, Hkv=1, d=8, stride=8 << 20, Q=None) == -1
