@@ -87,8 +87,9 @@ int dsa_page_append(const void* k, const void* v, const int64_t* slots, int T, i
  * Attention of new queries over all cached tokens.
  *   Q [total_q, Hq, d] bf16 or fp32; out the same shape and type
  *   q_offsets [B+1] int32: request b owns rows q_offsets[b] ..
- *          q_offsets[b+1] - 1 (m_b of them, 0 <= m_b <= max_q); rows at or
- *          behind q_offsets[B] are padding: their outputs stay as they were
+ *          q_offsets[b+1] - 1 (m_b of them, 0 <= m_b <= max_q); rows in front
+ *          of q_offsets[0] and from q_offsets[B] on belong to none: their
+ *          outputs stay as they were
  *   lens [B] int32: tokens of request b, its new ones included
  *   Query row j of request b sits at position lens[b] - m_b + j and sees the
  *   tokens up to and including it; head h reads key head h / (Hq / Hkv):

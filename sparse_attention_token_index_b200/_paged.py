@@ -329,7 +329,9 @@ def dsa_attend_paged(Q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tens
     Request b's m_b <= ``max_q`` query rows sit at its last m_b positions and
     see the tokens up to their own.  Returns out (Q's shape and type), with
     ``return_lse`` also the log-sum-exp [total_q, Hq] fp32.  A query that sees
-    nothing has out 0 and lse -inf; rows behind q_offsets[B] stay as they were.
+    nothing has out 0 and lse -inf; rows in front of q_offsets[0] and from
+    q_offsets[B] on are not written: they stay as they were in ``out`` and
+    ``lse``, and are not set in outputs that are allocated here.
     """
     return _attend("dsa_attend_paged", Q, K_pages, V_pages, block_table, lens, q_offsets, None, int(max_q), scale,
                    K_scale, V_scale, out, True if return_lse and lse is None else lse, workspace, stream, check)

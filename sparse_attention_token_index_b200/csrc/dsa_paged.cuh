@@ -62,7 +62,7 @@ __device__ __forceinline__ RowSeq row_of(const AttendArgs& a, int lo, int row) {
 // Finds the request whose rows hold `row` (offsets ascend; a request without
 // rows is passed over).
 __device__ __forceinline__ RowSeq find_row(const AttendArgs& a, int row) {
-  if (row >= a.q_off[a.B]) return RowSeq{-1, 0, -1};  // padding behind the last request
+  if (row < a.q_off[0] || row >= a.q_off[a.B]) return RowSeq{-1, 0, -1};  // in front of the first request, or padding
   int lo = 0, hi = a.B - 1;                            // the last b with q_off[b] <= row
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

@@ -1,5 +1,5 @@
 """Paged-cache calls on the GPU at their edges: references that move while
-other outputs wait, empty steps."""
+other outputs wait, empty steps, rows of no request."""
 import pytest
 import torch
 
@@ -105,3 +105,24 @@ def test_plan_of_no_requests_into_prepared_outputs(in_place):
         torch.cuda.synchronize()
         assert got is out
         assert out[0].tolist() == [0] and out[1].tolist() == [-1] * 5 and out[2].tolist() == [-1] * 5 and out[4].tolist() == [3]
+
+
+# ---------------------------------------------------------------------------
+# rows of no request
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("k", [None, 70])
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("e4m3", 64), ("fp32", 64), ("bf16", 136)])
+def test_rows_in_front_of_the_first_request(kv, d, k):
+    # some requests of a larger batch: their offsets start behind 0, and rows of the others stay as they were
+    step = Step([50, 300, 129, 7], [2, 1, 3, 1], 8, 2, d, kv, k=k, pad=2, seed=4)
+    want, wl = run(step)
+    ws = torch.zeros(32 << 20, dtype=torch.uint8, device=DEV)
+    out, lse = torch.full_like(step.Q, 7.0), torch.full(step.Q.shape[:2], 7.0, device=DEV)
+    step.table, step.lens_t, step.q_off = step.table[1:3].contiguous(), step.lens_t[1:3].contiguous(), step.q_off[1:4].contiguous()
+    run(step, out, lse, workspace=ws)
+    # within the rounding of sums cut at other places: both are within check's bound, and equal where nothing is cut
+    assert torch.allclose(out[2:6].float(), want[2:6].float(), atol=0.02, rtol=0.02)
+    assert torch.allclose(lse[2:6], wl[2:6], atol=1e-4, rtol=0)
+    for x in (out, lse):
+        assert torch.all(x[:2] == 7) and torch.all(x[6:] == 7)
+    dsa.dsa_check_status(ws)
