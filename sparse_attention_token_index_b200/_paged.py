@@ -98,6 +98,13 @@ def _pool(K, V, K_scale, V_scale, device, Hkv, d) -> Tuple[int, int]:
     return code, stride
 
 
+def _no_gradients(name: str, *tensors) -> None:
+    """None of the tensors wants a gradient that the call would lose."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{name} has no backward pass, and a tensor given to it requires a gradient: detach it, or call "
+                           "under torch.no_grad()")
+
+
 _same = contextlib.nullcontext()
 _EXT = None
 
@@ -241,6 +248,7 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
             return _check(r, "dsa_page_append")
     if k.dim() != 3:
         raise ValueError("k must be [T, Hkv, d]")
+    _no_gradients("dsa_page_append", k, v, K_pages, V_pages)
     dev, shape = k.device, k.shape
     T, Hkv, d = shape
     sd = _type(k, "k", False)
@@ -273,6 +281,7 @@ def _attend(name, Q, K, V, block_table, lens, q_offsets, idx, max_q, scale, K_sc
     if Q.dim() != 3 or K.dim() != 4 or lens.dim() != 1 or block_table.dim() != 2 or (idx is not None and idx.dim() != 2):
         raise ValueError("Q must be [total_q, Hq, d], K_pages [n_pages, page, Hkv, d], lens [B], block_table "
                          "[B, max_pages], idx [total_q, k]")
+    _no_gradients(name, Q, K, V, K_scale, V_scale)
     dev, dtype, shape, i32 = Q.device, Q.dtype, Q.shape, torch.int32
     rows, Hq, d = shape
     n_pages, page, Hkv, _ = K.shape
@@ -324,7 +333,8 @@ def dsa_attend_paged(Q: torch.Tensor, K_pages: torch.Tensor, V_pages: torch.Tens
     """Attention of new queries over every cached token.
 
     Q [total_q, Hq, d] bf16/fp32; pages [n_pages, page, Hkv, d] of the same
-    type, or e4m3 with scales [n_pages, page, Hkv]; block_table [B, max_pages],
+    type, or e4m3 with scales [n_pages, page, Hkv]; none of them may require a
+    gradient (there is no backward pass); block_table [B, max_pages],
     lens [B] (new tokens included), q_offsets [B+1], all int32 on the device.
     Request b's m_b <= ``max_q`` query rows sit at its last m_b positions and
     see the tokens up to their own.  Returns out (Q's shape and type), with

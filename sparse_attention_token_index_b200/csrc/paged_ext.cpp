@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -76,6 +77,15 @@ bool small(const at::Tensor& t) {  // every extent is an int
   for (const int64_t n : t.sizes())
     if (n > 0x7fffffff) return false;
   return true;
+}
+
+// Whether one of the tensors wants a gradient, which the calls would lose.
+template <size_t N>
+bool wants_gradient(const at::Tensor* (&t)[N]) {
+  if (!at::GradMode::is_enabled()) return false;
+  for (const at::Tensor* x : t)
+    if (x && x->requires_grad()) return true;
+  return false;
 }
 
 bool on_current_device(const at::Tensor& t) {
@@ -151,7 +161,7 @@ PyObject* page_append(const at::Tensor* (&t)[8]) {
   const at::Tensor &k = *t[0], &K = *t[1], &slots = *t[2], &ws = *t[7];
   int src = 0, type = 0;
   int64_t stride = 0;
-  if (k.dim() != 3 || !on_current_device(k) || !query_type(k, src) || !small(k) || (t[3] == nullptr) != (t[4] == nullptr))
+  if (wants_gradient(t) || k.dim() != 3 || !on_current_device(k) || !query_type(k, src) || !small(k) || (t[3] == nullptr) != (t[4] == nullptr))
     Py_RETURN_NONE;
   const c10::Device dev = k.device();
   if (k.size(0) < 1 || !k.is_contiguous() || (t[3] && !is(*t[3], k.scalar_type(), dev, k.sizes())) ||
@@ -170,7 +180,7 @@ PyObject* attend(const at::Tensor* (&t)[10], int max_q, const float* scale, bool
   const at::Tensor* idx = t[6];
   int qt = 0, type = 0;
   int64_t stride = 0;
-  if (Q.dim() != 3 || lens.dim() != 1 || table.dim() != 2 || (idx && idx->dim() != 2) || !on_current_device(Q) ||
+  if (wants_gradient(t) || Q.dim() != 3 || lens.dim() != 1 || table.dim() != 2 || (idx && idx->dim() != 2) || !on_current_device(Q) ||
       !query_type(Q, qt) || !small(Q) || !small(table) || K.dim() != 4)
     Py_RETURN_NONE;
   const c10::Device dev = Q.device();

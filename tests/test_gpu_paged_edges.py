@@ -1,5 +1,6 @@
 """Paged-cache calls on the GPU at their edges: references that move while
-other outputs wait, empty steps, rows of no request."""
+other outputs wait, empty steps, rows of no request,
+tensors that want a gradient."""
 import pytest
 import torch
 
@@ -126,3 +127,27 @@ def test_rows_in_front_of_the_first_request(kv, d, k):
     for x in (out, lse):
         assert torch.all(x[:2] == 7) and torch.all(x[6:] == 7)
     dsa.dsa_check_status(ws)
+
+
+# ---------------------------------------------------------------------------
+# gradients
+# ---------------------------------------------------------------------------
+def test_calls_refuse_tensors_that_want_a_gradient():
+    step = Step([40, 9], [1, 2], 4, 2, 64, "bf16", k=8)
+    ws = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
+    rows, slots = torch.randn((2, 2, 64), device=DEV).bfloat16(), torch.tensor([1, 2], device=DEV)
+    for kw in ({}, {"workspace": ws}):
+        for i in range(3):
+            a = list(step.args())
+            a[i] = a[i].detach().clone().requires_grad_()
+            for call in (lambda: dsa.dsa_attend_paged(*a, step.max_q, **kw), lambda: dsa.dsa_attend_selected(*a, step.idx, **kw)):
+                with pytest.raises(RuntimeError, match="gradient"):
+                    call()
+                with torch.no_grad():
+                    call()
+        with pytest.raises(RuntimeError, match="gradient"):
+            dsa.dsa_page_append(rows.clone().requires_grad_(), step.K, slots, v=rows, V_pages=step.V, **kw)
+        with pytest.raises(RuntimeError, match="gradient"):
+            dsa.dsa_page_append(rows, step.K, slots, v=rows.clone().requires_grad_(), V_pages=step.V, **kw)
+        with torch.no_grad():
+            dsa.dsa_page_append(rows.clone().requires_grad_(), step.K, slots, v=rows, V_pages=step.V, **kw)

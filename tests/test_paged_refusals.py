@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import sparse_attention_token_index_b200 as dsa
-from test_paged_api import BF16, E4M3, OK, _attend, _plan
+from test_paged_api import BF16, E4M3, OK, _attend, _cpu, _plan
 
 
 @pytest.fixture(scope="module")
@@ -64,3 +64,21 @@ def test_attention_refuses_tables_whose_last_tiles_pass_31_bits(L, selected):
     # the largest that is taken goes on to the next check
     assert _attend(L, selected, page=(1 << 31) - 1024, max_pages=1, Hq=1, Hkv=1, d=8, stride=((1 << 31) - 1024) * 8, Q=None) == -1
     assert _attend(L, selected, page=1 << 20, max_pages=(1 << 11) - 1, Hq=1, Hkv=1, d=8, stride=8 << 20, Q=None) == -1
+
+
+# ---------------------------------------------------------------------------
+# gradients
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("workspace", [None, torch.zeros(4096, dtype=torch.uint8)])
+def test_calls_without_a_backward_pass_refuse_tensors_that_want_a_gradient(workspace):
+    t = _cpu()
+    for name in ("Q", "K"):
+        a = {**t, name: t[name].clone().requires_grad_()}
+        for call in (lambda: dsa.dsa_attend_paged(a["Q"], a["K"], a["K"], a["table"], a["lens"], a["q"], 1, workspace=workspace),
+                     lambda: dsa.dsa_attend_selected(a["Q"], a["K"], a["K"], a["table"], a["lens"], a["q"], a["idx"],
+                                                     workspace=workspace),
+                     lambda: dsa.dsa_page_append(a["Q"][:, :2], a["K"], torch.zeros(2, dtype=torch.int64), workspace=workspace)):
+            with pytest.raises(RuntimeError, match="gradient"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA|on "):  # the next check
+                call()
