@@ -98,6 +98,12 @@ def _pool(K, V, K_scale, V_scale, device, Hkv, d) -> Tuple[int, int]:
     return code, stride
 
 
+def _ints(name: str, *sizes: int) -> None:
+    """Sizes that the library takes as 32-bit numbers (ctypes would cut others short without a word)."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"{name}: a size does not fit 32 bits: {list(sizes)}")
+
+
 def _no_gradients(name: str, *tensors) -> None:
     """None of the tensors wants a gradient that the call would lose."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
@@ -156,6 +162,7 @@ def _workspace(nbytes: int, device, workspace):
 @functools.lru_cache(maxsize=1024)
 def _bytes(name: str, device, *args) -> int:
     n = _sz(0)
+    _ints(name, *args)
     with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
         _check(getattr(lib(), name + "_workspace_size")(*args, ctypes.byref(n)), name)
     return int(n.value)
@@ -199,6 +206,7 @@ def dsa_page_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
         raise ValueError("lens must be [B], block_table [B, max_pages], free_pages [n_free]")
     B, i32 = lens.shape[0], torch.int32
     width, n_free, max_tokens = block_table.shape[1], free_pages.shape[0], int(max_tokens)
+    _ints("dsa_page_plan", B, width, n_free, int(page), int(n_pages), max_tokens)
     _need(lens, "lens", i32, (B,), dev)
     _need(new_lens, "new_lens", i32, (B,), dev)
     _need(block_table, "block_table", i32, (B, width), dev)
@@ -251,6 +259,7 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
     _no_gradients("dsa_page_append", k, v, K_pages, V_pages)
     dev, shape = k.device, k.shape
     T, Hkv, d = shape
+    _ints("dsa_page_append", *shape, *K_pages.shape)
     sd = _type(k, "k", False)
     _need(k, "k", k.dtype, shape, dev)
     if (v is None) != (V_pages is None):
@@ -285,6 +294,7 @@ def _attend(name, Q, K, V, block_table, lens, q_offsets, idx, max_q, scale, K_sc
     dev, dtype, shape, i32 = Q.device, Q.dtype, Q.shape, torch.int32
     rows, Hq, d = shape
     n_pages, page, Hkv, _ = K.shape
+    _ints(name, *shape, *K.shape, *lens.shape, *block_table.shape, max_q, *(() if idx is None else idx.shape))
     qd = _type(Q, "Q", False)
     _need(Q, "Q", dtype, shape, dev)
     kd, stride = _pool(K, V, K_scale, V_scale, dev, Hkv, d)

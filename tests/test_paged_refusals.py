@@ -66,6 +66,29 @@ def test_attention_refuses_tables_whose_last_tiles_pass_31_bits(L, selected):
     assert _attend(L, selected, page=1 << 20, max_pages=(1 << 11) - 1, Hq=1, Hkv=1, d=8, stride=8 << 20, Q=None) == -1
 
 
+@pytest.mark.parametrize("workspace", [None, torch.zeros(4096, dtype=torch.uint8)])
+@pytest.mark.parametrize("kw", [{"page": (1 << 32) + 16}, {"n_pages": (1 << 32) + 4}, {"max_tokens": (1 << 32) + 8}, {"page": 16 - (1 << 32)}])
+def test_plan_refuses_sizes_beyond_32_bits(workspace, kw):
+    t = _cpu()
+    a = {"page": 16, "n_pages": 4, "max_tokens": 8, **kw}
+    with pytest.raises(ValueError, match="32 bits"):
+        dsa.dsa_page_plan(t["lens"], t["lens"], t["table"], t["lens"], t["lens"][:1], workspace=workspace, **a)
+
+
+def test_other_calls_refuse_sizes_beyond_32_bits():
+    t, meta = _cpu(), dict(dtype=torch.bfloat16, device="meta")
+    many = torch.empty(((1 << 32) + 4, 16, 2, 64), **meta)
+    for call in (lambda: dsa.dsa_attend_paged(t["Q"], t["K"], t["K"], t["table"], t["lens"], t["q"], (1 << 32) + 1),
+                 lambda: dsa.dsa_attend_paged(t["Q"], many, many, t["table"], t["lens"], t["q"], 1),
+                 lambda: dsa.dsa_attend_selected(t["Q"], many, many, t["table"], t["lens"], t["q"], t["idx"]),
+                 lambda: dsa.dsa_page_append(torch.empty(((1 << 32) + 2, 2, 64), **meta), t["K"], t["q"].long()),
+                 lambda: dsa.dsa_page_append(t["Q"][:, :2], many, t["lens"].long()),
+                 lambda: dsa.page_plan_workspace_bytes(2, (1 << 32) + 8),
+                 lambda: dsa._paged._bytes("dsa_attend_paged", None, (1 << 32) + 1, 1, 1, 8, 2, 64, 0, 0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
 # ---------------------------------------------------------------------------
 # gradients
 # ---------------------------------------------------------------------------
