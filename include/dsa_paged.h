@@ -76,7 +76,8 @@ int dsa_page_plan(const int32_t* lens, const int32_t* new_lens, const int32_t* f
  *   v, V   may both be NULL (a cache of keys alone, such as the indexer's)
  *   src_dtype bf16 or fp32; kv_dtype the same, or e4m3, which stores
  *          scale = max(amax over d / 448, 2^-126) in K_scale / V_scale and
- *          e4m3(x / scale), rounded to nearest even.
+ *          e4m3(x / scale), rounded to nearest even.  A row and head that
+ *          holds an infinity or a NaN gets a scale of NaN, and reads back so.
  *   d <= 256.  T = 0 is an empty call.  The workspace needs 256 bytes.
  * ---------------------------------------------------------------------- */
 int dsa_page_append(const void* k, const void* v, const int64_t* slots, int T, int Hkv, int d, int src_dtype,

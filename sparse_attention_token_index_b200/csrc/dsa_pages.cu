@@ -344,6 +344,20 @@ __device__ __forceinline__ float divide(float x, float scale, float inv, bool ex
   return fmaf(fmaf(-q, scale, x), inv, q);
 }
 
+// The larger of two; NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Scale of a row whose largest magnitude is `top`; NaN where that is infinite
+// (by the correction of the quotient) or NaN, so that the row reads back as
+// NaN and an overflow is not lost.
+__device__ __forceinline__ float row_scale(float top) {
+  return max_nan(divide(top, 448.f, 1.f / 448.f, false), 1.17549435e-38f);
+}
+
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
   x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
@@ -398,9 +412,9 @@ __global__ void __launch_bounds__(256) append_e4m3_kernel(const AppendArgs a, in
     for (int i = 0; i < kAt; ++i) {
       float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) top = fmaxf(top, fabsf(x[i][e]));
-      for (int o = lanes >> 1; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float scale = fmaxf(divide(top, 448.f, 1.f / 448.f, false), 1.17549435e-38f), inv = __frcp_rn(scale);
+      for (int e = 0; e < kE; ++e) top = max_nan(top, fabsf(x[i][e]));
+      for (int o = lanes >> 1; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float scale = row_scale(top), inv = __frcp_rn(scale);
       const int64_t row = slot_row(a, slot[i]);
       if (row < 0) continue;
       if (scale < 0x1p-100f || (__float_as_uint(scale) & 0x7fffffu) == 0x7fffffu) {
@@ -457,11 +471,11 @@ __global__ void __launch_bounds__(256) append_e4m3_any_kernel(const AppendArgs a
     for (int i = 0; i < 8; ++i) {
       const int e = lane + 32 * i;
       x[i] = e < a.d ? (float)src[r * a.d + e] : 0.f;
-      top = fmaxf(top, fabsf(x[i]));
+      top = max_nan(top, fabsf(x[i]));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float scale = fmaxf(__fdiv_rn(top, 448.f), 1.17549435e-38f);
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float scale = row_scale(top);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = lane + 32 * i;

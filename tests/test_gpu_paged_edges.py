@@ -1,11 +1,12 @@
 """Paged-cache calls on the GPU at their edges: references that move while
 other outputs wait, empty steps, rows of no request,
-tensors that want a gradient."""
+tensors that want a gradient, values that are not finite."""
+import numpy as np
 import pytest
 import torch
 
 import sparse_attention_token_index_b200 as dsa
-from paged import DEV, Step, check
+from paged import DEV, TYPES, Step, check
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +152,30 @@ def test_calls_refuse_tensors_that_want_a_gradient():
             dsa.dsa_page_append(rows, step.K, slots, v=rows.clone().requires_grad_(), V_pages=step.V, **kw)
         with torch.no_grad():
             dsa.dsa_page_append(rows.clone().requires_grad_(), step.K, slots, v=rows, V_pages=step.V, **kw)
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("src", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [128, 24, 7])  # 16, 8 and one element a lane
+def test_append_e4m3_shows_what_is_not_finite(src, d):
+    """A row that holds an infinity or a NaN reads back as NaN, all of it, whatever the alignment; rows beside it are as
+    without it."""
+    gen = torch.Generator().manual_seed(d)
+    x = torch.randn((9, 2, d), generator=gen)
+    x[1, 0, d // 2] = float("inf")
+    x[3, 1, 0] = float("-inf")
+    x[4, 0, d - 1] = float("nan")
+    x[6, 1, 1], x[6, 1, 2] = float("nan"), float("inf")
+    x = x.to(TYPES[src]).to(DEV)
+    K = torch.zeros((9, 1, 2, d), dtype=torch.float8_e4m3fn, device=DEV)
+    sc = torch.zeros((9, 1, 2), device=DEV)
+    dsa.dsa_page_append(x, K, torch.arange(9, device=DEV), K_scale=sc, check=True)
+    got = K.float()[:, 0] * sc[:, 0, :, None]
+    bad = ~torch.isfinite(x.float()).all(-1)
+    assert int(bad.sum()) == 4 and torch.all(got[bad].isnan()) and torch.all(sc[:, 0][bad].isnan())
+    good = x.float()[~bad]
+    want = (good.cpu().abs().amax(-1) / np.float32(448)).clamp(min=2.0 ** -126)
+    assert torch.equal(sc[:, 0][~bad].cpu(), want)
+    assert torch.equal(K[:, 0][~bad].view(torch.uint8).cpu(), (good.cpu() / want[:, None]).to(torch.float8_e4m3fn).view(torch.uint8))
