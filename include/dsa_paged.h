@@ -96,6 +96,8 @@ int dsa_page_append(const void* k, const void* v, const int64_t* slots, int T, i
  *   tokens up to and including it; head h reads key head h / (Hq / Hkv):
  *       out[j, h] = sum_s p_s v_s,  p = softmax_s(scale * q[j, h] . k_s)
  *   A query that sees no token has out 0 and lse -inf.
+ *   (A NaN in a query row, or in a key or scale that it reads, shows in its
+ *   outputs and lse.)
  *   softmax_scale: HOST pointer to the scale, NULL for d^-1/2
  *   lse [total_q, Hq] fp32: log sum_s exp(scale q . k_s), or NULL
  *   Checked on the device: 0 <= lens[b] <= max_pages * page, offsets that

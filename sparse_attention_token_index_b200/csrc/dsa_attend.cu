@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
         const float k = __shfl_sync(0xffffffffu, ks, (j0 + 4 * i + grp) & 31);
         w[i] = __shfl_sync(0xffffffffu, vs, (j0 + 4 * i + grp) & 31);
         s[i] = p[i] >= 0 ? s[i] * k : -INFINITY;
-        top = fmaxf(top, s[i]);
+        top = max_nan(top, s[i]);
       }
       if (top == -INFINITY) continue;  // nothing seen yet (the same in the group's lanes)
-      if (top > m) {
+      if (!(top <= m)) {  // a larger maximum, or a NaN, which then stays
         const float keep = expf(m - top);
         m = top;
         l *= keep;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
   // the groups' sums, joined pairwise
 #pragma unroll
   for (int x = 8; x <= 16; x <<= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, x), l2 = __shfl_xor_sync(0xffffffffu, l, x), top = fmaxf(m, m2);
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, x), l2 = __shfl_xor_sync(0xffffffffu, l, x), top = max_nan(m, m2);
     const float f = m == -INFINITY ? 0.f : expf(m - top), f2 = m2 == -INFINITY ? 0.f : expf(m2 - top);
     m = top;
     l = l * f + l2 * f2;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
     if (warp > 0) return;
     float top = sm[0];
 #pragma unroll
-    for (int w = 1; w < kShare; ++w) top = fmaxf(top, sm[w]);
+    for (int w = 1; w < kShare; ++w) top = max_nan(top, sm[w]);
     l = 0.f;
 #pragma unroll
     for (int i = 0; i < kD; ++i) o[i] = 0.f;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
     m = top;
   }
   const bool last = splits == 1;
-  const float inv = last ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+  const float inv = last ? inverse(l) : 1.f;
   if (grp == 0) {
 #pragma unroll
     for (int i = 0; i < kD; ++i) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
   }
   if (lane == 0) {
     if (last) {
-      if (a.lse != nullptr) a.lse[rh] = l > 0.f ? m + logf(l) : -INFINITY;
+      if (a.lse != nullptr) a.lse[rh] = l == 0.f ? -INFINITY : m + logf(l);
     } else {
       a.part_ml[2 * task] = m;
       a.part_ml[2 * task + 1] = l;
@@ -222,17 +222,17 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a, in
   if (find_row(a, (int)(rh / a.Hq)).b < 0) return;
   const float* ml = a.part_ml + 2 * rh * splits;
   float top = -INFINITY, sum = 0.f;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, ml[2 * s]);
+  for (int s = 0; s < splits; ++s) top = max_nan(top, ml[2 * s]);
   for (int s = 0; s < splits; ++s)
     if (ml[2 * s] != -INFINITY) sum = fmaf(expf(ml[2 * s] - top), ml[2 * s + 1], sum);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = inverse(sum);
   for (int e = lane; e < a.d; e += 32) {
     float x = 0.f;
     for (int s = 0; s < splits; ++s)
       if (ml[2 * s] != -INFINITY) x = fmaf(expf(ml[2 * s] - top), a.part_o[(rh * splits + s) * a.d + e], x);
     put(static_cast<TQ*>(a.out) + rh * a.d + e, x * inv);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[rh] = sum > 0.f ? top + logf(sum) : -INFINITY;
+  if (lane == 0 && a.lse != nullptr) a.lse[rh] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 template <typename TQ, typename TK, int kD>

@@ -1106,12 +1106,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         pend_par = seg % C::kOBufs;
         pend_phase = (seg / C::kOBufs) & 1;
         pend_row = orow;
-        pend_inv = sum > 0.f ? 1.f / sum : 0.f;
+        pend_inv = inverse(sum);
         if (wg == 0) {
           if (!pend_whole) {
             reinterpret_cast<float4*>(a.part_ml)[pend_part * N + r] = make_float4(-nref, sum, sum, 0.f);
           } else if (a.lse != nullptr && orow >= 0) {
-            a.lse[orow] = sum > 0.f ? (log2f(sum) - nref) * 0.693147181f : -INFINITY;
+            a.lse[orow] = sum == 0.f ? -INFINITY : (log2f(sum) - nref) * 0.693147181f;
           }
         }
         ++seg;
@@ -1423,11 +1423,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           if (!pend_whole) {
             // a row without tokens here says so: it may share a reference far above its own scores elsewhere
             reinterpret_cast<float4*>(a.part_ml)[pend_part * N + r] =
-                make_float4(sum > 0.f ? -S.nref[r] : kNoMax, sum, rounded, 0.f);
+                make_float4(sum == 0.f ? kNoMax : -S.nref[r], sum, rounded, 0.f);
           } else if (a.lse != nullptr && S.orow[pend_par][r] >= 0) {
-            a.lse[S.orow[pend_par][r]] = sum > 0.f ? (log2f(sum) - S.nref[r]) * 0.693147181f : -INFINITY;
+            a.lse[S.orow[pend_par][r]] = sum == 0.f ? -INFINITY : (log2f(sum) - S.nref[r]) * 0.693147181f;
           }
-          S.lsum[pend_par][r] = rounded > 0.f ? 1.f / rounded : 0.f;
+          S.lsum[pend_par][r] = inverse(rounded);
         }
         named_bar(bar, 128);  // the rows' state is free for the next segment
         ++seg;
@@ -1531,7 +1531,7 @@ __global__ void __launch_bounds__(128) attend_tc_join_kernel(const AttendArgs a,
     }
   }
   if (r0 + warp >= d.rows) return;
-  const float inv = sum.lr > 0.f ? 1.f / sum.lr : 0.f;
+  const float inv = inverse(sum.lr);
   const int g = a.Hq / a.Hkv, rr = d.row0 + r0 + warp, j = rr / g;
   const int64_t orow = (int64_t)(d.q0 + j) * a.Hq + d.hk * g + (rr - j * g);
 #pragma unroll
@@ -1539,7 +1539,7 @@ __global__ void __launch_bounds__(128) attend_tc_join_kernel(const AttendArgs a,
     const int e = lane * kPer + i;
     if (e < a.d) *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * a.d + e) = pack_bf16(sum.o[i] * inv, sum.o[i + 1] * inv);
   }
-  if (lane == 0 && a.lse != nullptr) a.lse[orow] = sum.l > 0.f ? (sum.m + log2f(sum.l)) * 0.693147181f : -INFINITY;
+  if (lane == 0 && a.lse != nullptr) a.lse[orow] = sum.l == 0.f ? -INFINITY : (sum.m + log2f(sum.l)) * 0.693147181f;
 }
 
 // ----------------------------------------------------------------------------

@@ -74,6 +74,16 @@ __device__ __forceinline__ RowSeq find_row(const AttendArgs& a, int row) {
   return row_of(a, lo, row);
 }
 
+// The larger of two; NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 1 / sum of a softmax, 0 for a row that sees nothing; a NaN stays one.
+__device__ __forceinline__ float inverse(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }
+
 // a / b (a >= 0, b > 0); the 32-bit division is several times shorter.
 __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;

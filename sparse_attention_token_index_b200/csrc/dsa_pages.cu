@@ -344,13 +344,6 @@ __device__ __forceinline__ float divide(float x, float scale, float inv, bool ex
   return fmaf(fmaf(-q, scale, x), inv, q);
 }
 
-// The larger of two; NaN if either is one.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Scale of a row whose largest magnitude is `top`; NaN where that is infinite
 // (by the correction of the quotient) or NaN, so that the row reads back as
 // NaN and an overflow is not lost.

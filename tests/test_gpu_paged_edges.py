@@ -179,3 +179,30 @@ def test_append_e4m3_shows_what_is_not_finite(src, d):
     want = (good.cpu().abs().amax(-1) / np.float32(448)).clamp(min=2.0 ** -126)
     assert torch.equal(sc[:, 0][~bad].cpu(), want)
     assert torch.equal(K[:, 0][~bad].view(torch.uint8).cpu(), (good.cpu() / want[:, None]).to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+@pytest.mark.parametrize("k", [None, 150])
+@pytest.mark.parametrize("kv,d,Hq", [("bf16", 128, 8), ("bf16", 64, 64), ("bf16", 128, 100), ("e4m3", 128, 8), ("e4m3", 64, 64),
+                                     ("e4m3", 128, 128), ("fp32", 64, 8), ("bf16", 136, 8)])
+def test_attention_shows_what_is_not_finite(kv, d, Hq, k):
+    """A NaN in one query row, or in a key that a request's rows read, comes out as NaN in outputs and log-sum-exp; other
+    requests stay as they are."""
+    lens, news = [300, 140, 520], [1, 1, 1]
+    step = Step(lens, news, Hq, 1, d, kv, page=16, k=k, seed=5)
+    want, wl = run(step)
+    step.Q[1] = float("nan")
+    out, lse = run(step)
+    assert torch.all(out[1].isnan()) and torch.all(lse[1].isnan())
+    for r in (0, 2):
+        assert torch.equal(out[r], want[r]) and torch.equal(lse[r], wl[r])
+    step = Step(lens, news, Hq, 1, d, kv, page=16, k=k, seed=5)
+    pos = 130 if k is None else int(step.idx[2][step.idx[2] >= 0][77])
+    at = (int(step.table[2, pos // 16]), pos % 16)
+    if kv == "e4m3":
+        step.scales[0][at] = float("nan")
+    else:
+        step.K[at] = float("nan")
+    out, lse = run(step)
+    assert torch.all(out[2].isnan()) and torch.all(lse[2].isnan())
+    for r in (0, 1):
+        assert torch.equal(out[r], want[r]) and torch.equal(lse[r], wl[r])
