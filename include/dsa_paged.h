@@ -96,14 +96,16 @@ int dsa_page_append(const void* k, const void* v, const int64_t* slots, int T, i
  *   tokens up to and including it; head h reads key head h / (Hq / Hkv):
  *       out[j, h] = sum_s p_s v_s,  p = softmax_s(scale * q[j, h] . k_s)
  *   A query that sees no token has out 0 and lse -inf.
- *   (A NaN in a query row, or in a key or scale that it reads, shows in its
- *   outputs and lse.)
+ *   A NaN in a query row, or in a key or scale that it reads, shows in its
+ *   outputs and lse; only an e4m3 NaN byte under a finite scale, which the
+ *   cache write never leaves, may read as a number.
  *   softmax_scale: HOST pointer to the scale, NULL for d^-1/2
  *   lse [total_q, Hq] fp32: log sum_s exp(scale q . k_s), or NULL
  *   Checked on the device: 0 <= lens[b] <= max_pages * page, offsets that
- *   ascend within 0 .. total_q, m_b <= max_q; a request that fails is
- *   skipped, a page id outside the pool hides its tokens, and either records
- *   DSA_ERR_INVALID_ARG (the outputs of such a call are unspecified).
+ *   ascend within 0 .. total_q, m_b <= max_q, page ids within the pool.  A
+ *   request that fails is skipped, nothing outside the pool is read, and
+ *   either records DSA_ERR_INVALID_ARG (the outputs of such a call are
+ *   unspecified).
  *   Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 128, d <= 256,
  *   1 <= max_q <= 65536, max_pages * page <= 2^31 - 1024.  fp32 queries
  *   take fp32 pages, bf16 queries bf16 or e4m3 pages.
@@ -121,7 +123,9 @@ int dsa_attend_paged(const void* Q, const void* K, const void* V, const float* K
  * Attention of queries over the positions the indexer chose for them.
  *   idx [total_q, k] int32: positions local to the row's request, as the
  *          dsa_index_* calls answer them.  An entry below 0 or beyond the
- *          row's own position is skipped; one that stands twice counts twice.
+ *          row's own position is skipped, and one whose page id lies outside
+ *          the pool (which is also recorded); one that stands twice counts
+ *          twice.
  *   All else as for dsa_attend_paged, without max_q: a request may own any
  *   number of rows (a whole prompt).  1 <= k <= 65536.
  * ---------------------------------------------------------------------- */

@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             S.vsc[tk][i * 32 + lane] = vs[i];
           }
           if constexpr (kSel) {
-            const uint32_t seen = __ballot_sync(0xffffffffu, pos[i] >= 0);
+            const uint32_t seen = __ballot_sync(0xffffffffu, row[i] >= 0);
             if (lane == 0) S.seen[tk][i] = seen;
           }
         }

@@ -206,3 +206,24 @@ def test_attention_shows_what_is_not_finite(kv, d, Hq, k):
     assert torch.all(out[2].isnan()) and torch.all(lse[2].isnan())
     for r in (0, 1):
         assert torch.equal(out[r], want[r]) and torch.equal(lse[r], wl[r])
+
+
+# ---------------------------------------------------------------------------
+# pages outside the pool
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kv,d,Hq", [("bf16", 128, 8), ("bf16", 64, 64), ("bf16", 128, 100), ("e4m3", 128, 8), ("fp32", 64, 8),
+                                     ("bf16", 136, 8)])
+def test_list_entries_in_pages_outside_the_pool_are_skipped(kv, d, Hq):
+    step = Step([300, 129], [2, 1], Hq, Hq // 8 if Hq == 8 else 1, d, kv, page=16, k=100, seed=3)
+    ws = torch.zeros(32 << 20, dtype=torch.uint8, device=DEV)
+    table = step.table
+    step.table = table.clone()
+    step.table[0, 2:5] = i32([-1, 1 << 29, step.K.shape[0]])
+    out, lse = run(step, workspace=ws, check=False)
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_check_status(ws)
+    assert e.value.status == -1
+    idx = step.idx.clone()
+    idx[:2] = torch.where((idx[:2] >= 32) & (idx[:2] < 80), -1, idx[:2])
+    step.table, step.idx = table, idx
+    check(step, out, lse)
