@@ -2,13 +2,15 @@
 
 A plain call (on the current device and stream, outputs allocated here, with a
 workspace) goes through the ``_paged_ext`` extension; every other one, and any
-whose arguments do not pass, through the checks below and ctypes.
+whose arguments do not pass, through the checks below and ctypes.  Both reach
+the same library call; where the extension is missing all go the second way.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
 import functools
+import warnings
 from typing import Optional, Tuple
 
 import torch
@@ -118,7 +120,7 @@ _EXT = None
 def _ext():
     """The extension, bound to the loaded library; raises if it has not been built."""
     global _EXT
-    if _EXT is None:
+    if not _EXT:
         try:
             from . import _paged_ext
         except ImportError as e:
@@ -128,6 +130,21 @@ def _ext():
         _paged_ext.bind(*(ctypes.cast(getattr(L, n), _vp).value for n in EXPORTED_SYMBOLS))
         _EXT = _paged_ext
     return _EXT
+
+
+def _plain():
+    """The extension for plain calls; None where it cannot be imported (said once)."""
+    global _EXT
+    if _EXT is None:
+        try:
+            from . import _paged_ext  # noqa: F401
+        except ImportError as e:
+            warnings.warn(f"_paged_ext cannot be imported ({e}): paged calls take a few microseconds longer on the host; build it "
+                          "with `python -m sparse_attention_token_index_b200.build`", RuntimeWarning, stacklevel=3)
+            _EXT = False
+        else:
+            _ext()
+    return _EXT or None
 
 
 def _on(device: torch.device, stream):
@@ -197,8 +214,8 @@ def dsa_page_plan(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch
     few free pages (DSA_ERR_PAGES) or lengths out of range fail as a whole:
     the table stays, the step has no tokens, and the status word tells.
     """
-    if out is None and stream is None and not check and workspace is not None:
-        r = (_EXT or _ext()).page_plan(lens, new_lens, block_table, free_pages, used, page, n_pages, max_tokens, workspace)
+    if out is None and stream is None and not check and workspace is not None and (ext := _EXT or _plain()):
+        r = ext.page_plan(lens, new_lens, block_table, free_pages, used, page, n_pages, max_tokens, workspace)
         if r is not None:
             return r if type(r) is tuple else _check(r, "dsa_page_plan")
     dev = lens.device
@@ -250,8 +267,8 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
     each token and head: scale = max(amax / 448, 2^-126).  ``v`` and
     ``V_pages`` may be left out (a cache of keys alone).
     """
-    if stream is None and not check and workspace is not None:
-        r = (_EXT or _ext()).page_append(k, K_pages, slots, v, V_pages, K_scale, V_scale, workspace)
+    if stream is None and not check and workspace is not None and (ext := _EXT or _plain()):
+        r = ext.page_append(k, K_pages, slots, v, V_pages, K_scale, V_scale, workspace)
         if r is not None:
             return _check(r, "dsa_page_append")
     if k.dim() != 3:
@@ -282,9 +299,9 @@ def dsa_page_append(k: torch.Tensor, K_pages: torch.Tensor, slots: torch.Tensor,
 
 def _attend(name, Q, K, V, block_table, lens, q_offsets, idx, max_q, scale, K_scale, V_scale, out, lse, workspace,
             stream, check):
-    if out is None and stream is None and not check and workspace is not None and (lse is None or lse is True):
-        r = (_EXT or _ext()).attend(Q, K, V, block_table, lens, q_offsets, idx, K_scale, V_scale, workspace, max_q, scale,
-                                    lse is True)
+    if out is None and stream is None and not check and workspace is not None and (lse is None or lse is True) \
+            and (ext := _EXT or _plain()):
+        r = ext.attend(Q, K, V, block_table, lens, q_offsets, idx, K_scale, V_scale, workspace, max_q, scale, lse is True)
         if r is not None:
             return _check(r, name) if type(r) is int else r
     if Q.dim() != 3 or K.dim() != 4 or lens.dim() != 1 or block_table.dim() != 2 or (idx is not None and idx.dim() != 2):
