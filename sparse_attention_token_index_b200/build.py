@@ -6,7 +6,7 @@ arch=compute_100a,code=sm_100a``) in parallel and linked into one shared
 library next to this file; the CUDA runtime is linked statically, so the
 library loads without a GPU (only calls into it need one).  ``csrc/paged_ext.cpp``
 becomes ``_paged_ext.so``, the Python extension that hands torch tensors to the
-library's paged-cache calls.
+library's paged-cache calls; the library is built first and does without it.
 
 ``--debug-bounds`` builds ``libdsa_index_debug.so`` instead: the same
 library compiled with ``-DDSA_DEBUG_BOUNDS=1``, whose kernels check every
@@ -20,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -87,10 +88,17 @@ def build_ext(force: bool = False) -> str:
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=None, debug_bounds: bool = False) -> str:
-    build_ext(force and not debug_bounds)
     lib = DEBUG_LIB if debug_bounds else LIB
-    if not force and up_to_date(lib):
-        return lib
+    if force or not up_to_date(lib):
+        _build_lib(lib, verbose, extra_flags, debug_bounds)
+    try:
+        build_ext(force and not debug_bounds)
+    except (RuntimeError, OSError, ImportError) as e:  # no C++ compiler, no Python headers, no torch
+        warnings.warn(f"{os.path.basename(lib)} is built, the Python extension is not: {e}", RuntimeWarning, stacklevel=2)
+    return lib
+
+
+def _build_lib(lib: str, verbose: bool, extra_flags, debug_bounds: bool) -> None:
     build_dir = BUILD + ("_debug" if debug_bounds else "")
     os.makedirs(build_dir, exist_ok=True)
     nvcc = _nvcc()
@@ -119,7 +127,6 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None, debug_bo
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":

@@ -1,11 +1,13 @@
 """The Python extension of the paged calls: what a machine without it still
 has, and when it is built (CPU)."""
+import subprocess
 import sys
 
 import pytest
 import torch
 
 import sparse_attention_token_index_b200 as dsa
+from sparse_attention_token_index_b200 import build as B
 from test_paged_api import _cpu
 
 
@@ -32,3 +34,33 @@ def test_calls_do_without_the_extension(monkeypatch):
                 call()
     with pytest.raises(RuntimeError, match="build it"):
         dsa._paged._ext()
+
+
+@pytest.fixture
+def commands(monkeypatch, tmp_path):
+    """The compiler commands that a build would run; their outputs are empty files in a folder of the test's own."""
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    for name in ("LIB", "DEBUG_LIB", "EXT", "BUILD"):
+        monkeypatch.setattr(B, name, str(tmp_path / name))
+    monkeypatch.setattr(B.subprocess, "run", run)
+    return ran
+
+
+def test_the_library_is_built_first_and_without_the_extension(monkeypatch, commands):
+    monkeypatch.setenv("CXX", "the-c++-compiler")
+    assert B.build() == B.LIB
+    assert commands[-1][0] == "the-c++-compiler" and all(c[0] != "the-c++-compiler" for c in commands[:-1]) and len(commands) > 2
+    done = len(commands)
+    assert B.build() == B.LIB and len(commands) == done  # up to date
+
+    def fails(force=False):
+        raise FileNotFoundError("the-c++-compiler")
+    monkeypatch.setattr(B, "build_ext", fails)
+    with pytest.warns(RuntimeWarning, match="extension"):
+        assert B.build(force=True) == B.LIB
+    assert len(commands) > done
