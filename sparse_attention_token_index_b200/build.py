@@ -65,10 +65,8 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def build_ext(force: bool = False) -> str:
-    """Compiles the Python extension against the installed torch."""
-    deps = [EXT_SRC, os.path.join(INCLUDE, "dsa_paged.h"), os.path.join(INCLUDE, "dsa_index.h"), __file__]
-    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in deps):
-        return EXT
+    """Compiles the Python extension against the installed torch: anew when a source has changed, and for another
+    torch or Python than it was built for (a binary of one loads, or fails, in the other)."""
     import sysconfig
 
     import torch
@@ -80,10 +78,21 @@ def build_ext(force: bool = False) -> str:
            "-I" + sysconfig.get_paths()["include"], f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
            f"-I{cuda}/include", EXT_SRC, "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_cuda"]
+    deps = [EXT_SRC, os.path.join(INCLUDE, "dsa_paged.h"), os.path.join(INCLUDE, "dsa_index.h"), __file__]
+    key = f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}\n"
+    key_file = os.path.join(BUILD, "paged_ext.key")
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in deps):
+        if os.path.exists(key_file):
+            with open(key_file) as f:
+                if f.read() == key:
+                    return EXT
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(key_file, "w") as f:
+        f.write(key)
     return EXT
 
 

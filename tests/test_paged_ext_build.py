@@ -64,3 +64,13 @@ def test_the_library_is_built_first_and_without_the_extension(monkeypatch, comma
     with pytest.warns(RuntimeWarning, match="extension"):
         assert B.build(force=True) == B.LIB
     assert len(commands) > done
+
+
+def test_the_extension_is_built_anew_for_another_torch(monkeypatch, commands):
+    B.build_ext()
+    B.build_ext()
+    assert len(commands) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    B.build_ext()
+    B.build_ext()
+    assert len(commands) == 2
