@@ -86,7 +86,7 @@ int dsa_version(void);
 
 /* Failure-path control, for tests of the bounded waits (ADIndex — Deployment
  * Guidance: a fallback path is only trustworthy once it has been exercised).
- * Every wait of the tensor-core kernel is bounded: when it runs out, the
+ * Every wait of the tensor-core kernels is bounded: when one runs out, the
  * kernel records DSA_ERR_TIMEOUT in the status word, lets the copies and MMAs
  * it already issued land, frees its tensor memory and returns, so the device
  * stays usable.  `budget_us` sets the time budget, in microseconds, of the
@@ -94,8 +94,9 @@ int dsa_version(void);
  * (0 restores the default of 2 s; the final drain of issued work always
  * keeps the default).
  * With `hold_first_tile` nonzero, the first CTA of the following dense-kind
- * launches never loads its first key tile, so the wait for it runs out and
- * that launch reports DSA_ERR_TIMEOUT (its outputs are then unspecified).
+ * launches, and of the tensor-core attention launches of dsa_paged.h, never
+ * loads its first key tile, so the wait for it runs out and that launch
+ * reports DSA_ERR_TIMEOUT (its outputs are then unspecified).
  * Process-wide, read at each launch; call it between calls, never while
  * another thread launches.  Returns DSA_OK. */
 int dsa_debug_set_wait(unsigned int budget_us, int hold_first_tile);

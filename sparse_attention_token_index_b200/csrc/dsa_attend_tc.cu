@@ -83,7 +83,10 @@ struct TcAttend {
   int64_t run;          // chosen positions: tiles of one CTA
   int min_run;          // all tokens: least tiles of one CTA
   struct JoinDesc* desc;
+  // failure-path controls (dsa_debug_set_wait; zero in normal calls): the time
+  // budget of the waits (0 = the default), and a first tile that CTA 0 never posts
   uint64_t wait_ns;
+  int hold_first_tile;
 };
 
 // What the join kernel needs of the unit a CTA's run begins in.
@@ -758,7 +761,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.tok_full[tk]);
+        if (lane == 0 && !(t.hold_first_tile && blockIdx.x == 0 && n == 0)) mbar_arrive(&S.tok_full[tk]);
       }
     }
     if (n % kLookWarps == lw) {  // the end, for the copy warps
@@ -1635,6 +1638,7 @@ int run_attend_tc(const AttendArgs& args, int kv_dtype, int rows, int sms, uint8
   off += round256((size_t)sms * 2 * N * 16);
   t.a.part_o = reinterpret_cast<float*>(ws + off);
   t.row_stride_page = (int)(args.page_stride / args.d);
+  wait_controls(t.wait_ns, t.hold_first_tile);
   int grid = sms;
   t.min_run = 2;
   if (args.idx != nullptr) {

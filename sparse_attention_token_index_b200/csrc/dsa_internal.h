@@ -115,9 +115,11 @@ TimerSlot timer_acquire();
 
 int launch_tc_index(const CUtensorMap& tmQ, const CUtensorMap& tmK, const TcArgs& a, int grid,
                     cudaStream_t stream);
-// dsa_debug_set_wait: time budget (microseconds) of the tensor-core kernel's
-// inter-role waits (0 = default) and the held first tile of the failure-path test.
+// dsa_debug_set_wait: time budget (microseconds) of the tensor-core kernels'
+// inter-role waits (0 = default) and the held first tile of the failure-path
+// tests; what a launch reads of them, the budget in ns.
 void set_wait_controls(uint32_t budget_us, int hold_first_tile);
+void wait_controls(uint64_t& budget_ns, int& hold_first_tile);
 size_t tc_smem_bytes();
 
 // Exact fp32 CUDA-core path (any H <= 128, d <= 256, H*d <= 8192).

@@ -728,6 +728,11 @@ void set_wait_controls(uint32_t budget_us, int hold_first_tile) {
   g_hold_first_tile.store(hold_first_tile ? 1 : 0);
 }
 
+void wait_controls(uint64_t& budget_ns, int& hold_first_tile) {
+  budget_ns = (uint64_t)g_wait_us.load() * 1000u;
+  hold_first_tile = g_hold_first_tile.load();
+}
+
 int launch_tc_index(const CUtensorMap& tmQ, const CUtensorMap& tmK, const TcArgs& args, int grid,
                     cudaStream_t stream) {
   static const char* const kNames[5] = {"dsa.score_topk.prefill", "dsa.score_topk.decode",
@@ -735,8 +740,7 @@ int launch_tc_index(const CUtensorMap& tmQ, const CUtensorMap& tmK, const TcArgs
                                          "dsa.score_topk.ivf_refine"};
   const NvtxRange nvtx(args.kind >= 0 && args.kind <= 4 ? kNames[args.kind] : "dsa.score_topk");
   TcArgs a = args;
-  a.wait_ns = (uint64_t)g_wait_us.load() * 1000u;
-  a.hold_first_tile = g_hold_first_tile.load();
+  wait_controls(a.wait_ns, a.hold_first_tile);
   if (a.kind < 0 || a.kind > 4 || (a.dbg_scores != nullptr && a.kind != 0)) return DSA_ERR_INVALID_ARG;
   const TimerSlot ts = timer_acquire();
   if (ts.start) cudaEventRecord(ts.start, stream);

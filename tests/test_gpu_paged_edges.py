@@ -1,6 +1,6 @@
 """Paged-cache calls on the GPU at their edges: references that move while
 other outputs wait, empty steps, rows of no request,
-tensors that want a gradient, values that are not finite."""
+tensors that want a gradient, values that are not finite, waits that run out."""
 import numpy as np
 import pytest
 import torch
@@ -227,3 +227,31 @@ def test_list_entries_in_pages_outside_the_pool_are_skipped(kv, d, Hq):
     idx[:2] = torch.where((idx[:2] >= 32) & (idx[:2] < 80), -1, idx[:2])
     step.table, step.idx = table, idx
     check(step, out, lse)
+
+
+# ---------------------------------------------------------------------------
+# the bounded waits
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("k", [None, 300])
+@pytest.mark.parametrize("kv,Hq", [("bf16", 8), ("bf16", 64), ("bf16", 128), ("e4m3", 8), ("e4m3", 64), ("e4m3", 128)])
+def test_a_wait_that_runs_out_is_reported(kv, Hq, k):
+    """The first CTA never posts its first tile (dsa_debug_set_wait): the wait for it runs out, all roles leave, and the
+    launch says so; the same workspace then serves a call whose results match the oracle."""
+    step = Step([3000, 700], [1, 1], Hq, 1, 128, kv, page=32, k=k, seed=2)
+    ws = torch.zeros(32 << 20, dtype=torch.uint8, device=DEV)
+    dsa.dsa_debug_set_wait(2000, hold_first_tile=True)
+    try:
+        run(step, workspace=ws, check=False)
+        with pytest.raises(dsa.DsaError) as e:
+            dsa.dsa_check_status(ws)
+        assert e.value.status == -5
+    finally:
+        dsa.dsa_debug_set_wait(0, hold_first_tile=False)
+    torch.cuda.synchronize()
+    check(step, *run(step, workspace=ws))
+    # a budget far above any wait of a working launch changes nothing
+    dsa.dsa_debug_set_wait(20000)
+    try:
+        check(step, *run(step, workspace=ws))
+    finally:
+        dsa.dsa_debug_set_wait(0)
