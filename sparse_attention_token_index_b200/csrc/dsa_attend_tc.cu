@@ -441,6 +441,7 @@ struct Cfg {
   // Registers a thread: launched with 72 (28 warps), of which the copy warps
   // give some up, so that the softmax warps hold a row's or token's scores.
   static constexpr int kSoftRegs = kFp8 ? 128 : 144, kMidRegs = 56, kCopyRegs = kFp8 ? 48 : 40;
+  static_assert(kSoftWarps % 4 == 0 && (1 + kLookWarps) % 4 == 0 && kCopyWarps % 4 == 0, "roles that share a number of registers fill warpgroups");
   static_assert(256 * kSoftRegs + 128 * kMidRegs + 512 * kCopyRegs <= kWarps * 32 * kLaunchRegs, "the registers of the launch");
   // Tensor memory: two score tiles; with rows on the lanes the weights, two
   // tiles or one and its rests (64 columns each); two output tiles, one where
@@ -658,243 +659,244 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     }
-  } else if (warp > kMma) {
-    // ---------------- lookup warps: positions -> cache rows, masks, scales; queries ----------------
-    set_regs<C::kMidRegs, false>();
-    const int lw = warp - kMma - 1;
-    Walk<N, kSel> walk;
-    walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
-    Seg s;
-    int n = 0, qn = 0;  // tiles, segments
-    bool ok = true;
-    auto tile_free = [&]() {
-      ok = ok && mbar_wait<true>(&S.tok_empty[n % kTok], ((n / kTok) & 1) ^ 1, abort_flag, a.status, 73, budget);
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    while (ok && walk.next(t, s)) {
-      if (!s.valid) continue;
-      // the segment's queries, a third each; the first segment's by two warps, as the third looks up its first tile
-      const bool split3 = qn > 0;
-      const int qb = qn % C::kQBufs;
-      if (qn >= C::kQBufs)
-        ok = mbar_wait<true>(&S.q_empty[qb], (qn / C::kQBufs - 1) & 1, abort_flag, a.status, 70, budget);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const uint8_t* Q = static_cast<const uint8_t*>(a.Q);
-      constexpr int kQUnits = D / 8;
-#pragma unroll 2
-      for (int e = (split3 ? lw : (lw > 0 ? lw - 1 : N * kQUnits)) * 32 + lane; e < N * kQUnits;
-           e += (split3 ? kLookWarps : kLookWarps - 1) * 32) {
-        const int r = e / kQUnits, u = e % kQUnits;
-        // rows behind the last repeat the first, so that their scores move no reference
-        const int rr = s.row0 + (r < s.rows ? r : 0), j = rr / g;
-        const bool in = u * 8 < a.d;
-        const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
-        uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
-        if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (in) v = *reinterpret_cast<const uint4*>(Q + at * 2);
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                         __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
-        } else {
-          copy16(smem_u32(dst), Q + at * 2, in);
-        }
-      }
-      if constexpr (kFp8) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.q_full[qb]);
-      } else {
-        copies_arrive(&S.q_full[qb]);
-      }
-      ++qn;
-      for (int j = 0; j < s.tiles; ++j, ++n) {
-        if (n % kLookWarps != lw) continue;  // the tiles in turn
-        const int tk = n % kTok, e0 = (s.tile0 + j) * kTile + lane;
-        int pos[4], id[4], off[4], row[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = e0 + i * 32;
-          pos[i] = -1;
-          if (e < s.end) pos[i] = kSel ? a.idx[(int64_t)s.q0 * a.k + e] : e;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (kSel && pos[i] > s.lim0) pos[i] = -1;
-          id[i] = -1;
-          off[i] = 0;
-          if (pos[i] >= 0) {
-            const int col = (int)((unsigned)pos[i] / (unsigned)a.page);
-            off[i] = pos[i] - col * a.page;
-            id[i] = a.table[(int64_t)s.b * a.max_pages + col];
-          }
-        }
-        float ks[4], vs[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          row[i] = -1;
-          ks[i] = vs[i] = 0.f;
-          if ((unsigned)id[i] < (unsigned)a.n_pages) {
-            row[i] = id[i] * t.row_stride_page + off[i] * a.Hkv + s.hk;
-            if constexpr (kFp8) {
-              const int64_t at = ((int64_t)id[i] * a.page + off[i]) * a.Hkv + s.hk;
-              ks[i] = a.K_scale[at];
-              vs[i] = a.V_scale[at];
-            }
-          } else if (pos[i] >= 0) {
-            report_error(a.status, DSA_ERR_INVALID_ARG, 41);
-          }
-        }
-        tile_free();
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          S.rows[tk][i * 32 + lane] = row[i];
-          if constexpr (kFp8) {
-            S.ksc[tk][i * 32 + lane] = ks[i] * (a.scale * 1.44269504f);
-            S.vsc[tk][i * 32 + lane] = vs[i];
-          }
-          if constexpr (kSel) {
-            const uint32_t seen = __ballot_sync(0xffffffffu, row[i] >= 0);
-            if (lane == 0) S.seen[tk][i] = seen;
-          }
-        }
-        __syncwarp();
-        if (lane == 0 && !(t.hold_first_tile && blockIdx.x == 0 && n == 0)) mbar_arrive(&S.tok_full[tk]);
-      }
-    }
-    if (n % kLookWarps == lw) {  // the end, for the copy warps
-      tile_free();
-      if (ok) {
-        if (lane == 0) {
-          S.rows[n % kTok][0] = kEnd;
-          mbar_arrive(&S.tok_full[n % kTok]);
-        }
-        __syncwarp();
-      }
-    }
-    if (lw == 0) {  // what the join needs of the unit this run begins in
-      JoinDesc d;
-      d.rows = 0;
-      d.run = run;
-      d.first = d.last = begin;
-      d.q0 = d.hk = d.row0 = 0;
-      if (n_tiles > 0) {
-        walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
-        walk.next(t, s);
-        d.rows = s.valid ? s.rows : 0;
-        d.first = begin - s.tile0;
-        d.last = d.first + s.unit_tiles;
-        d.q0 = s.q0;
-        d.hk = s.hk;
-        d.row0 = s.row0;
-      }
-      if (lane == 0) t.desc[blockIdx.x] = d;
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMma) {
-    // ---------------- MMA issuer: the warp waits, one lane issues ----------------
-    set_regs<C::kMidRegs, false>();
-    Walk<N, kSel> walk;
-    walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
-    Seg s;
-    constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
-    constexpr uint32_t kIdescO = C::kRows ? idesc_bf16_f32(128, D) | (1u << 16)                // V along N
-                                          : idesc_bf16_f32(D, C::kPCols) | (1u << 15) | (1u << 16);  // V^T along M, P along N
-    const bool leader = elect_one();
-    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(S.ring[0])), vdesc = mnmajor_desc<128>(smem_u32(S.ring[0]), kTile * 128);
-    const uint64_t qdesc = sw128_kmajor_desc(smem_u32(S.q[0])), pdesc = mnmajor_desc<C::kPRow>(smem_u32(S.p[0]), kTile * 128);
-    int n = 0, seg = 0;  // tiles, segments
-    int slot = 0;        // ring slot of the next K tile
-    uint32_t ring_phase = 0;
-    bool ok = true, pending = false, pend_first = false, pend_last = false;
-    int pend_slot = 0, pend_seg = 0;
-    uint32_t pend_phase = 0;
-    auto values = [&](int i) {  // the output tile += weights x V of tile i
-      const int pb = i & 1, par = pend_seg % C::kOBufs;
-      ok = mbar_wait(&S.full[pend_slot], pend_phase, abort_flag, a.status, 80, budget) &&
-           mbar_wait(&S.p_full[pb], (i >> 1) & 1, abort_flag, a.status, 81, budget) &&
-           (!pend_first || pend_seg < C::kOBufs ||
-            mbar_wait(&S.o_free[par], (pend_seg / C::kOBufs - 1) & 1, abort_flag, a.status, 82, budget));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      fence_async_smem();  // the loaders' copies, before the matrix unit reads them
-      tc_fence_after();
-      if (leader) {
-        const uint64_t v = vdesc + (uint64_t)(pend_slot * (C::kSlotBytes >> 4));
-        const uint64_t p = pdesc + (uint64_t)(i % C::kPBufs * (C::kPBytes >> 4));
-        const uint32_t o = tmem_base + C::kOCol + par * C::kOCols, ps = tmem_base + C::kPCol + (C::kPBufs == 2 ? pb * 64 : 0);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          const uint64_t vk = v + (uint64_t)(k * (2048 >> 4));
-          if constexpr (C::kRows) {
-            tc_mma_bf16_ts(o, ps + k * 8, vk, kIdescO, !(pend_first && k == 0));
-            if constexpr (C::kSplit) tc_mma_bf16_ts(o, ps + 64 + k * 8, vk, kIdescO, 1);
-          } else {
-            tc_mma_bf16(o, vk, p + (uint64_t)(k * C::kPRow), kIdescO, !(pend_first && k == 0));
-          }
-        }
-        tc_commit(&S.empty[pend_slot]);
-        tc_commit(&S.p_empty[pb]);
-        if (pend_last) tc_commit(&S.o_full[par]);
-      }
-      __syncwarp();
-    };
-    auto step = [&]() {
-      if (++slot == C::kSlots) {
-        slot = 0;
-        ring_phase ^= 1;
-      }
-    };
-    while (ok && walk.next(t, s)) {
-      if (!s.valid) continue;
-      const int qb = seg % C::kQBufs;
-      ok = mbar_wait(&S.q_full[qb], (seg / C::kQBufs) & 1, abort_flag, a.status, 83, budget);
-      ok = __all_sync(0xffffffffu, ok);
-      for (int j = 0; ok && j < s.tiles; ++j, ++n) {
-        ok = mbar_wait(&S.full[slot], ring_phase, abort_flag, a.status, 84, budget);
+  } else if (warp >= kMma) {
+    set_regs<C::kMidRegs, false>();  // the warps of a warpgroup change theirs by one instruction, ahead of their roles
+    if (warp > kMma) {
+      // ---------------- lookup warps: positions -> cache rows, masks, scales; queries ----------------
+      const int lw = warp - kMma - 1;
+      Walk<N, kSel> walk;
+      walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+      Seg s;
+      int n = 0, qn = 0;  // tiles, segments
+      bool ok = true;
+      auto tile_free = [&]() {
+        ok = ok && mbar_wait<true>(&S.tok_empty[n % kTok], ((n / kTok) & 1) ^ 1, abort_flag, a.status, 73, budget);
+        ok = __all_sync(0xffffffffu, ok);
+      };
+      while (ok && walk.next(t, s)) {
+        if (!s.valid) continue;
+        // the segment's queries, a third each; the first segment's by two warps, as the third looks up its first tile
+        const bool split3 = qn > 0;
+        const int qb = qn % C::kQBufs;
+        if (qn >= C::kQBufs)
+          ok = mbar_wait<true>(&S.q_empty[qb], (qn / C::kQBufs - 1) & 1, abort_flag, a.status, 70, budget);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        // the score tile is free: the weights of tile n - 2 were waited for below
-        fence_async_smem();
+        const uint8_t* Q = static_cast<const uint8_t*>(a.Q);
+        constexpr int kQUnits = D / 8;
+#pragma unroll 2
+        for (int e = (split3 ? lw : (lw > 0 ? lw - 1 : N * kQUnits)) * 32 + lane; e < N * kQUnits;
+             e += (split3 ? kLookWarps : kLookWarps - 1) * 32) {
+          const int r = e / kQUnits, u = e % kQUnits;
+          // rows behind the last repeat the first, so that their scores move no reference
+          const int rr = s.row0 + (r < s.rows ? r : 0), j = rr / g;
+          const bool in = u * 8 < a.d;
+          const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
+          uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
+          if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (in) v = *reinterpret_cast<const uint4*>(Q + at * 2);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                           __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+          } else {
+            copy16(smem_u32(dst), Q + at * 2, in);
+          }
+        }
+        if constexpr (kFp8) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.q_full[qb]);
+        } else {
+          copies_arrive(&S.q_full[qb]);
+        }
+        ++qn;
+        for (int j = 0; j < s.tiles; ++j, ++n) {
+          if (n % kLookWarps != lw) continue;  // the tiles in turn
+          const int tk = n % kTok, e0 = (s.tile0 + j) * kTile + lane;
+          int pos[4], id[4], off[4], row[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = e0 + i * 32;
+            pos[i] = -1;
+            if (e < s.end) pos[i] = kSel ? a.idx[(int64_t)s.q0 * a.k + e] : e;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (kSel && pos[i] > s.lim0) pos[i] = -1;
+            id[i] = -1;
+            off[i] = 0;
+            if (pos[i] >= 0) {
+              const int col = (int)((unsigned)pos[i] / (unsigned)a.page);
+              off[i] = pos[i] - col * a.page;
+              id[i] = a.table[(int64_t)s.b * a.max_pages + col];
+            }
+          }
+          float ks[4], vs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            row[i] = -1;
+            ks[i] = vs[i] = 0.f;
+            if ((unsigned)id[i] < (unsigned)a.n_pages) {
+              row[i] = id[i] * t.row_stride_page + off[i] * a.Hkv + s.hk;
+              if constexpr (kFp8) {
+                const int64_t at = ((int64_t)id[i] * a.page + off[i]) * a.Hkv + s.hk;
+                ks[i] = a.K_scale[at];
+                vs[i] = a.V_scale[at];
+              }
+            } else if (pos[i] >= 0) {
+              report_error(a.status, DSA_ERR_INVALID_ARG, 41);
+            }
+          }
+          tile_free();
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            S.rows[tk][i * 32 + lane] = row[i];
+            if constexpr (kFp8) {
+              S.ksc[tk][i * 32 + lane] = ks[i] * (a.scale * 1.44269504f);
+              S.vsc[tk][i * 32 + lane] = vs[i];
+            }
+            if constexpr (kSel) {
+              const uint32_t seen = __ballot_sync(0xffffffffu, row[i] >= 0);
+              if (lane == 0) S.seen[tk][i] = seen;
+            }
+          }
+          __syncwarp();
+          if (lane == 0 && !(t.hold_first_tile && blockIdx.x == 0 && n == 0)) mbar_arrive(&S.tok_full[tk]);
+        }
+      }
+      if (n % kLookWarps == lw) {  // the end, for the copy warps
+        tile_free();
+        if (ok) {
+          if (lane == 0) {
+            S.rows[n % kTok][0] = kEnd;
+            mbar_arrive(&S.tok_full[n % kTok]);
+          }
+          __syncwarp();
+        }
+      }
+      if (lw == 0) {  // what the join needs of the unit this run begins in
+        JoinDesc d;
+        d.rows = 0;
+        d.run = run;
+        d.first = d.last = begin;
+        d.q0 = d.hk = d.row0 = 0;
+        if (n_tiles > 0) {
+          walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+          walk.next(t, s);
+          d.rows = s.valid ? s.rows : 0;
+          d.first = begin - s.tile0;
+          d.last = d.first + s.unit_tiles;
+          d.q0 = s.q0;
+          d.hk = s.hk;
+          d.row0 = s.row0;
+        }
+        if (lane == 0) t.desc[blockIdx.x] = d;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // ---------------- MMA issuer: the warp waits, one lane issues ----------------
+      Walk<N, kSel> walk;
+      walk.start(t, n_tiles, S.begin_b, kSel ? begin : S.begin_off);
+      Seg s;
+      constexpr uint32_t kIdescS = idesc_bf16_f32(128, N);
+      constexpr uint32_t kIdescO = C::kRows ? idesc_bf16_f32(128, D) | (1u << 16)                // V along N
+                                            : idesc_bf16_f32(D, C::kPCols) | (1u << 15) | (1u << 16);  // V^T along M, P along N
+      const bool leader = elect_one();
+      const uint64_t kdesc = sw128_kmajor_desc(smem_u32(S.ring[0])), vdesc = mnmajor_desc<128>(smem_u32(S.ring[0]), kTile * 128);
+      const uint64_t qdesc = sw128_kmajor_desc(smem_u32(S.q[0])), pdesc = mnmajor_desc<C::kPRow>(smem_u32(S.p[0]), kTile * 128);
+      int n = 0, seg = 0;  // tiles, segments
+      int slot = 0;        // ring slot of the next K tile
+      uint32_t ring_phase = 0;
+      bool ok = true, pending = false, pend_first = false, pend_last = false;
+      int pend_slot = 0, pend_seg = 0;
+      uint32_t pend_phase = 0;
+      auto values = [&](int i) {  // the output tile += weights x V of tile i
+        const int pb = i & 1, par = pend_seg % C::kOBufs;
+        ok = mbar_wait(&S.full[pend_slot], pend_phase, abort_flag, a.status, 80, budget) &&
+             mbar_wait(&S.p_full[pb], (i >> 1) & 1, abort_flag, a.status, 81, budget) &&
+             (!pend_first || pend_seg < C::kOBufs ||
+              mbar_wait(&S.o_free[par], (pend_seg / C::kOBufs - 1) & 1, abort_flag, a.status, 82, budget));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        fence_async_smem();  // the loaders' copies, before the matrix unit reads them
         tc_fence_after();
         if (leader) {
-          const uint64_t k = kdesc + (uint64_t)(slot * (C::kSlotBytes >> 4));
-          const uint64_t q = qdesc + (uint64_t)(qb * (C::kQBytes >> 4));
-          const uint32_t d = tmem_base + (n & 1) * C::kSCols;
+          const uint64_t v = vdesc + (uint64_t)(pend_slot * (C::kSlotBytes >> 4));
+          const uint64_t p = pdesc + (uint64_t)(i % C::kPBufs * (C::kPBytes >> 4));
+          const uint32_t o = tmem_base + C::kOCol + par * C::kOCols, ps = tmem_base + C::kPCol + (C::kPBufs == 2 ? pb * 64 : 0);
 #pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ko = k + (uint64_t)((c * kTile * 128 + kk * 32) >> 4);
-              const uint64_t qo = q + (uint64_t)((c * N * 128 + kk * 32) >> 4);
-              tc_mma_bf16(d, C::kRows ? qo : ko, C::kRows ? ko : qo, kIdescS, (c | kk) != 0);
+          for (int k = 0; k < kTile / 16; ++k) {
+            const uint64_t vk = v + (uint64_t)(k * (2048 >> 4));
+            if constexpr (C::kRows) {
+              tc_mma_bf16_ts(o, ps + k * 8, vk, kIdescO, !(pend_first && k == 0));
+              if constexpr (C::kSplit) tc_mma_bf16_ts(o, ps + 64 + k * 8, vk, kIdescO, 1);
+            } else {
+              tc_mma_bf16(o, vk, p + (uint64_t)(k * C::kPRow), kIdescO, !(pend_first && k == 0));
             }
-          tc_commit(&S.empty[slot]);
-          tc_commit(&S.s_full[n & 1]);
-          if (j == s.tiles - 1) tc_commit(&S.q_empty[qb]);
+          }
+          tc_commit(&S.empty[pend_slot]);
+          tc_commit(&S.p_empty[pb]);
+          if (pend_last) tc_commit(&S.o_full[par]);
         }
         __syncwarp();
-        step();
-        if (pending) values(n - 1);
-        pending = true;
-        pend_first = j == 0;
-        pend_last = j == s.tiles - 1;
-        pend_seg = seg;
-        pend_slot = slot;
-        pend_phase = ring_phase;
-        step();
+      };
+      auto step = [&]() {
+        if (++slot == C::kSlots) {
+          slot = 0;
+          ring_phase ^= 1;
+        }
+      };
+      while (ok && walk.next(t, s)) {
+        if (!s.valid) continue;
+        const int qb = seg % C::kQBufs;
+        ok = mbar_wait(&S.q_full[qb], (seg / C::kQBufs) & 1, abort_flag, a.status, 83, budget);
+        ok = __all_sync(0xffffffffu, ok);
+        for (int j = 0; ok && j < s.tiles; ++j, ++n) {
+          ok = mbar_wait(&S.full[slot], ring_phase, abort_flag, a.status, 84, budget);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // the score tile is free: the weights of tile n - 2 were waited for below
+          fence_async_smem();
+          tc_fence_after();
+          if (leader) {
+            const uint64_t k = kdesc + (uint64_t)(slot * (C::kSlotBytes >> 4));
+            const uint64_t q = qdesc + (uint64_t)(qb * (C::kQBytes >> 4));
+            const uint32_t d = tmem_base + (n & 1) * C::kSCols;
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t ko = k + (uint64_t)((c * kTile * 128 + kk * 32) >> 4);
+                const uint64_t qo = q + (uint64_t)((c * N * 128 + kk * 32) >> 4);
+                tc_mma_bf16(d, C::kRows ? qo : ko, C::kRows ? ko : qo, kIdescS, (c | kk) != 0);
+              }
+            tc_commit(&S.empty[slot]);
+            tc_commit(&S.s_full[n & 1]);
+            if (j == s.tiles - 1) tc_commit(&S.q_empty[qb]);
+          }
+          __syncwarp();
+          step();
+          if (pending) values(n - 1);
+          pending = true;
+          pend_first = j == 0;
+          pend_last = j == s.tiles - 1;
+          pend_seg = seg;
+          pend_slot = slot;
+          pend_phase = ring_phase;
+          step();
+        }
+        ++seg;
       }
-      ++seg;
+      if (ok && pending) values(n - 1);
+      // never leave with an MMA in flight
+      if (leader) {
+        tc_commit(&S.drain);
+        mbar_wait_drain(&S.drain, 0, a.status, 86);
+      }
+      __syncwarp();
     }
-    if (ok && pending) values(n - 1);
-    // never leave with an MMA in flight
-    if (leader) {
-      tc_commit(&S.drain);
-      mbar_wait_drain(&S.drain, 0, a.status, 86);
-    }
-    __syncwarp();
   } else {
     // ---------------- softmax ----------------
     set_regs<C::kSoftRegs, true>();
