@@ -9,9 +9,9 @@ becomes ``_paged_ext.so``, the Python extension that hands torch tensors to the
 library's paged-cache calls; the library is built first and does without it.
 
 ``--debug-bounds`` builds ``libdsa_index_debug.so`` instead: the same
-library compiled with ``-DDSA_DEBUG_BOUNDS=1``, whose kernels check every
-index they are about to use against its buffer and record a failing check in
-the status word (``DSA_LIB`` selects it at load time).
+library compiled with ``-DDSA_DEBUG_BOUNDS=1``, whose kernels check the
+indices that they compute for lists, caches, tables, partial results and
+outputs against those buffers and record a failing check in the status word (``DSA_LIB`` selects it at load time).
 """
 from __future__ import annotations
 

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(kGenWarps * 32) attend_general_kernel(const At
         const int id = page_of(a, rs.b, pos, off);
         if (id >= 0) {
           at = (int64_t)id * a.page_stride + ((int64_t)off * a.Hkv + hk) * a.d;
+          if (!in_bounds(cache_ok(a, at), a.status, 21)) at = -1;
           if (a.K_scale != nullptr) {
             const int64_t sc = ((int64_t)id * a.page + off) * a.Hkv + hk;
             ks = a.K_scale[sc];

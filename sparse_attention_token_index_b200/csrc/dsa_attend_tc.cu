@@ -110,6 +110,13 @@ struct Seg {
   bool valid;
 };
 
+// What the debug build checks ahead of an access (in_bounds): a cache row by its number, an output row, a part.
+__device__ __forceinline__ bool row_ok(const TcAttend& t, int row) { return cache_ok(t.a, (int64_t)row * t.a.d); }
+__device__ __forceinline__ bool out_ok(const AttendArgs& a, int64_t orow) {
+  return orow >= 0 && orow < (int64_t)a.total_q * a.Hq;
+}
+__device__ __forceinline__ bool part_ok(int64_t part, unsigned ctas) { return part >= 0 && part < 2 * (int64_t)ctas; }
+
 __device__ __forceinline__ bool request_ok(const AttendArgs& a, int b, int& q0, int& m, int& len) {
   q0 = a.q_off[b];
   const int q1 = a.q_off[b + 1];
@@ -606,7 +613,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
           const int row = rows[i];
-          const bool in = row >= 0 && unit_ok;
+          const bool in = row >= 0 && unit_ok && in_bounds(row_ok(t, row), a.status, 22);
           copy16(dst + i * 128 + (((unit & 7) ^ ((sub * kTimes + i) & 7)) << 4),
                  in ? pages + (uint64_t)(uint32_t)row * row_bytes : static_cast<const uint8_t*>(a.K), in);
         }
@@ -625,7 +632,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
             "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
             : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-            : "l"(pages + (uint64_t)(uint32_t)row * row_bytes), "r"((uint32_t)(row >= 0 && unit_ok)));
+            : "l"(pages + (uint64_t)(uint32_t)row * row_bytes),
+              "r"((uint32_t)(row >= 0 && unit_ok && in_bounds(row_ok(t, row), a.status, 22))));
       };
       // the second 64-element chunk's lanes write their odd unit first, so that no two lanes of a row share banks
       const int flip = (unit >> 2) & 1;
@@ -690,7 +698,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const int r = e / kQUnits, u = e % kQUnits;
           // rows behind the last repeat the first, so that their scores move no reference
           const int rr = s.row0 + (r < s.rows ? r : 0), j = rr / g;
-          const bool in = u * 8 < a.d;
+          const bool in = u * 8 < a.d && in_bounds(out_ok(a, (int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)), a.status, 23);
           const int64_t at = in ? ((int64_t)(s.q0 + j) * a.Hq + s.hk * g + (rr - j * g)) * a.d + u * 8 : 0;
           uint8_t* dst = S.q[qb] + (u >> 3) * N * 128 + r * 128 + (((u & 7) ^ (r & 7)) << 4);
           if constexpr (kFp8) {  // in the order of the converted keys: elements 0, 2, 1, 3 of every four
@@ -719,7 +727,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           for (int i = 0; i < 4; ++i) {
             const int e = e0 + i * 32;
             pos[i] = -1;
-            if (e < s.end) pos[i] = kSel ? a.idx[(int64_t)s.q0 * a.k + e] : e;
+            if (e < s.end && in_bounds(!kSel || (e < a.k && s.q0 < a.total_q), a.status, 24)) pos[i] = kSel ? a.idx[(int64_t)s.q0 * a.k + e] : e;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -729,7 +737,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             if (pos[i] >= 0) {
               const int col = (int)((unsigned)pos[i] / (unsigned)a.page);
               off[i] = pos[i] - col * a.page;
-              id[i] = a.table[(int64_t)s.b * a.max_pages + col];
+              if (in_bounds(table_ok(a, s.b, col), a.status, 25)) id[i] = a.table[(int64_t)s.b * a.max_pages + col];
             }
           }
           float ks[4], vs[4];
@@ -938,6 +946,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           tmem_ld_wait();
           if (!ok) continue;
           const int c = wg * kHalf + i0;
+          if (!in_bounds(pend_whole ? pend_row < 0 || out_ok(a, pend_row) : part_ok(pend_part, gridDim.x), a.status, 26)) continue;
           if (!pend_whole) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (pend_part * N + r) * D + c);
 #pragma unroll
@@ -1153,7 +1162,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         } else {
           tmem_ld_wait();
         }
-        if (ok && dv_ok) {
+        if (ok && dv_ok && in_bounds(pend_whole || part_ok(pend_part, gridDim.x), a.status, 27)) {
           if (!pend_whole) {
             float* dst = a.part_o + (pend_part * N + c0) * D + dv;
 #pragma unroll
@@ -1163,7 +1172,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
               const int r = S.orow[pend_par][c0 + i];
-              if (r >= 0) out[(int64_t)r * a.d] = __float2bfloat16_rn(v[i] * S.lsum[pend_par][c0 + i]);
+              if (r >= 0 && in_bounds(out_ok(a, r), a.status, 28)) out[(int64_t)r * a.d] = __float2bfloat16_rn(v[i] * S.lsum[pend_par][c0 + i]);
             }
           }
         }
@@ -1484,7 +1493,8 @@ __global__ void __launch_bounds__(128) attend_tc_join_kernel(const AttendArgs a,
   // parts: the end of run c0 (its only segment, or its last), then the beginnings of the others
   const int64_t slot0 = d.first == c0 * d.run ? 2 * c0 : 2 * c0 + 1;
   auto load = [&](int p, int r, float4& ml, float (&v)[kPer]) {  // lane l: elements kPer l .. kPer l + kPer - 1
-    const int64_t at = (p == 0 ? slot0 : 2 * (c0 + p)) * N + r0 + r;
+    int64_t at = (p == 0 ? slot0 : 2 * (c0 + p)) * N + r0 + r;
+    if (!in_bounds(part_ok(at / N, gridDim.x + 1), a.status, 29)) at = 0;
     ml = reinterpret_cast<const float4*>(a.part_ml)[at];
     if constexpr (kPer == 4) {
       const float4 x = reinterpret_cast<const float4*>(a.part_o + at * D)[lane];
@@ -1539,6 +1549,7 @@ __global__ void __launch_bounds__(128) attend_tc_join_kernel(const AttendArgs a,
   const float inv = inverse(sum.lr);
   const int g = a.Hq / a.Hkv, rr = d.row0 + r0 + warp, j = rr / g;
   const int64_t orow = (int64_t)(d.q0 + j) * a.Hq + d.hk * g + (rr - j * g);
+  if (!in_bounds(out_ok(a, orow), a.status, 30)) return;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2) {  // d is even here
     const int e = lane * kPer + i;

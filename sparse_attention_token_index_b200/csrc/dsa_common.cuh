@@ -34,7 +34,7 @@ __device__ __forceinline__ void report_error(int* status, int code, int info) {
 }
 
 // Debug bounds checks, compiled in by -DDSA_DEBUG_BOUNDS=1 (the library's
-// debug build, libdsa_index_debug.so): an index a kernel is about to use is
+// debug build, libdsa_index_debug.so): an index that a kernel is about to use is
 // checked against the extent of its buffer; a failing check records
 // DSA_ERR_INTERNAL with info 100 + site in the status word and the access is
 // skipped.  In the normal build in_bounds is constant true and costs nothing.

@@ -89,12 +89,21 @@ __device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
   return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// What the debug build checks ahead of an access (in_bounds): a table entry; a
+// cache row of d elements, at an element offset in the pool.
+__device__ __forceinline__ bool table_ok(const AttendArgs& a, int b, int col) {
+  return (unsigned)b < (unsigned)a.B && (unsigned)col < (unsigned)a.max_pages;
+}
+__device__ __forceinline__ bool cache_ok(const AttendArgs& a, int64_t at) {
+  return at >= 0 && at + a.d <= (a.n_pages - 1) * a.page_stride + (int64_t)a.page * a.Hkv * a.d;
+}
+
 // Page id of `pos` of request b (0 <= pos < len), -1 if the table names a
 // page outside the pool; `off` is the offset within the page.
 __device__ __forceinline__ int page_of(const AttendArgs& a, int b, int pos, int& off) {
   const int col = (int)((unsigned)pos / (unsigned)a.page);
   off = pos - col * a.page;
-  const int id = a.table[(int64_t)b * a.max_pages + col];
+  const int id = in_bounds(table_ok(a, b, col), a.status, 20) ? a.table[(int64_t)b * a.max_pages + col] : -1;
   if ((unsigned)id >= (unsigned)a.n_pages) {
     report_error(a.status, DSA_ERR_INVALID_ARG, 41);
     return -1;

@@ -161,7 +161,7 @@ __device__ __forceinline__ int bisect(const int32_t* off, int n, int x) {
 // Entry i of the pages handed out this step, -1 if the list names a page
 // outside the pool.
 __device__ __forceinline__ int fresh_page(const PlanArgs& a, int used, int i) {
-  const int id = a.free_pages[used + i];
+  const int id = in_bounds((unsigned)(used + i) < (unsigned)a.n_free, a.status, 31) ? a.free_pages[used + i] : -1;
   if ((unsigned)id < (unsigned)a.n_pages) return id;
   report_error(a.status, DSA_ERR_INVALID_ARG, 51);
   return -1;
@@ -176,7 +176,9 @@ __device__ __forceinline__ void plan_fill(const PlanArgs& a, const int32_t* q_of
     const int b = bisect(first, a.B, (int)i);
     const int len = lens[b] - (q_off[b + 1] - q_off[b]);
     const int held = pages_of(len, a.page);
-    a.table[(int64_t)b * a.max_pages + held + ((int)i - first[b])] = fresh_page(a, used, (int)i);
+    const int col = held + ((int)i - first[b]);
+    if (in_bounds((unsigned)col < (unsigned)a.max_pages, a.status, 32))
+      a.table[(int64_t)b * a.max_pages + col] = fresh_page(a, used, (int)i);
   }
   // A warp takes a run of tokens, one a lane and turn (a wider turn is more
   // code, and a step this short waits for its instructions); a lane's next
@@ -202,6 +204,7 @@ __device__ __forceinline__ void plan_fill(const PlanArgs& a, const int32_t* q_of
       pos = len + (int)i - q0;
       const int col = (int)((unsigned)pos / (unsigned)a.page);
       // the last page the request held already, or one of this step's
+      if (!in_bounds(b < a.B && col < a.max_pages && (col < held || used + first[b] + col - held < a.n_free), a.status, 33)) continue;
       const int id = *(col < held ? a.table + (int64_t)b * a.max_pages + col : a.free_pages + used + first[b] + col - held);
       if ((unsigned)id < (unsigned)a.n_pages)
         slot = (int64_t)id * a.page + (pos - col * a.page);
@@ -306,7 +309,9 @@ __device__ __forceinline__ int64_t slot_row(const AppendArgs& a, int64_t slot) {
     return -1;
   }
   const int64_t id = slot < ((int64_t)1 << 31) ? (unsigned)slot / (unsigned)a.page : slot / a.page;
-  return id * a.page_stride + (slot - id * a.page) * a.Hkv * a.d;
+  const int64_t row = id * a.page_stride + (slot - id * a.page) * a.Hkv * a.d;
+  const int64_t end = (a.n_pages - 1) * a.page_stride + (int64_t)a.page * a.Hkv * a.d;
+  return in_bounds(row >= 0 && row + (int64_t)a.Hkv * a.d <= end, a.status, 34) ? row : -1;
 }
 
 // Same type in source and pool: rows of `units` vectors of type V, a warp
