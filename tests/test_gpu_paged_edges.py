@@ -1,12 +1,14 @@
 """Paged-cache calls on the GPU at their edges: references that move while
-other outputs wait, empty steps, rows of no request,
-tensors that want a gradient, values that are not finite, waits that run out."""
+other outputs wait, weights in two parts, empty steps, rows of no request,
+tensors that want a gradient, pages outside the pool, values that are not
+finite, waits that run out."""
 import numpy as np
 import pytest
 import torch
 
 import sparse_attention_token_index_b200 as dsa
-from paged import DEV, TYPES, Step, check
+from paged import DEV, TYPES, Step, check, f64
+from paged_weights import TWO_PARTS, cancelling, two_parts_exceeded
 
 pytestmark = pytest.mark.gpu
 
@@ -87,6 +89,18 @@ def test_values_all_alike_come_out_as_they_are(kv, Hq, Hkv, m, d, k):
         assert float((out / v0.float() - 1).abs().max()) <= 2.0 ** -13
     else:
         assert torch.equal(out.float(), v0.float().expand_as(out))
+
+
+# ---------------------------------------------------------------------------
+# weights in two parts
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("k", [None, 150])
+@pytest.mark.parametrize("kv,Hq,Hkv,d", TWO_PARTS)
+def test_weights_of_more_than_bf16(kv, Hq, Hkv, d, k):
+    # up to 32 rows, and from e4m3, a weight goes in as two bf16 parts; on the CUDA cores it is fp32
+    step = cancelling(kv, Hq, Hkv, d, k)
+    bad = two_parts_exceeded(step, f64(run(step)[0]))
+    assert not bad.any(), np.argwhere(bad)[:4].tolist()
 
 
 # ---------------------------------------------------------------------------
