@@ -70,29 +70,25 @@ def build_ext(force: bool = False) -> str:
     import sysconfig
 
     import torch
+    deps = [EXT_SRC, os.path.join(INCLUDE, "dsa_paged.h"), os.path.join(INCLUDE, "dsa_index.h"), __file__]
+    key = f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}"  # stands in the binary, as the module's __doc__
+    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in deps):
+        with open(EXT, "rb") as f:
+            if key.encode() in f.read():
+                return EXT
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = EXT + ".tmp"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DDSA_BUILT_FOR="{key}"',
+           "-I" + INCLUDE,
            "-I" + sysconfig.get_paths()["include"], f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include",
            f"-I{cuda}/include", EXT_SRC, "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10",
            "-lc10_cuda"]
-    deps = [EXT_SRC, os.path.join(INCLUDE, "dsa_paged.h"), os.path.join(INCLUDE, "dsa_index.h"), __file__]
-    key = f"torch {torch.__version__} {sysconfig.get_config_var('SOABI')}\n"
-    key_file = os.path.join(BUILD, "paged_ext.key")
-    if not force and os.path.exists(EXT) and all(os.path.getmtime(p) <= os.path.getmtime(EXT) for p in deps):
-        if os.path.exists(key_file):
-            with open(key_file) as f:
-                if f.read() == key:
-                    return EXT
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
-    os.makedirs(BUILD, exist_ok=True)
-    with open(key_file, "w") as f:
-        f.write(key)
     return EXT
 
 

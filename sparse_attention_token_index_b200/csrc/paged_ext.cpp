@@ -273,7 +273,8 @@ PyMethodDef methods[] = {
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_attend)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_ext", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+// DSA_BUILT_FOR: the torch and Python of the build, by which the next one tells whether the binary fits
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_ext", DSA_BUILT_FOR, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 

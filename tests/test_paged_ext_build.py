@@ -38,12 +38,13 @@ def test_calls_do_without_the_extension(monkeypatch):
 
 @pytest.fixture
 def commands(monkeypatch, tmp_path):
-    """The compiler commands that a build would run; their outputs are empty files in a folder of the test's own."""
+    """The compiler commands that a build would run; what they would write goes into a folder of the test's own."""
     ran = []
 
     def run(cmd, **kw):
         ran.append(cmd)
-        open(cmd[cmd.index("-o") + 1], "w").close()
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("\n".join(cmd))
         return subprocess.CompletedProcess(cmd, 0, "", "")
     for name in ("LIB", "DEBUG_LIB", "EXT", "BUILD"):
         monkeypatch.setattr(B, name, str(tmp_path / name))
@@ -74,3 +75,9 @@ def test_the_extension_is_built_anew_for_another_torch(monkeypatch, commands):
     B.build_ext()
     B.build_ext()
     assert len(commands) == 2
+    monkeypatch.setattr(B, "_nvcc", lambda: 1 / 0)  # a binary that fits asks for no compiler
+    B.build_ext()
+
+
+def test_the_extension_says_what_it_was_built_for():
+    assert torch.__version__ in dsa._paged._ext().__doc__
