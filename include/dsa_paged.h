@@ -26,7 +26,8 @@
  * dsa_check_status); calls are asynchronous on `stream`, allocate nothing and
  * can be captured into a CUDA graph.  A workspace serves one call at a time.
  * Queries, keys and values must be finite in every slot below a request's
- * length; slots at or beyond it may hold anything.
+ * length, values below 2^80 in magnitude (sums are kept unnormalised); slots at
+ * or beyond it may hold anything.
  */
 #ifndef DSA_PAGED_H
 #define DSA_PAGED_H

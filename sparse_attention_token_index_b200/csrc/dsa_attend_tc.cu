@@ -11,9 +11,11 @@
 // and N/2 of its rows.  Beyond 64 rows (N = 128) the query rows fill the lanes
 // themselves, S = Q K^T and O += P V: a thread owns half a row, whose statistics
 // stay in its registers, and the weights are the A operand in tensor memory
-// (128 rows over 32 caches of 131072 tokens: 385 us, 901 with tokens on the
-// lanes).  Decoding reads each K and V row once for N rows, 2 N flops a byte,
-// and at N <= 128 memory is the bound.
+// (128 rows over 32 caches of 131072 tokens: 372 us, ten passes in a graph, 901
+// with tokens on the lanes).  Decoding reads each K and V row once for N rows,
+// 2 N flops a byte.  Few rows are bound by memory (64 ragged caches: 72 % of the
+// copy bandwidth); 64 and 128 by the softmax warps as soon as the power cap
+// lowers the clock, and e4m3 caches by their conversion.
 //
 // One persistent CTA per SM:
 //   * three lookup warps turn positions into cache rows (page table, or list
@@ -24,8 +26,8 @@
 //     whatever the page size; a token that no row sees, and the columns
 //     behind d, are filled with zeros, so no stale value meets a zero weight.
 //     One warp issues such a copy of scattered rows every 60 cycles or so:
-//     sixteen reach 17 TB/s from L2 and 7 TB/s from memory, eight 14.5 and
-//     5.7, four 8.7 and 3.3.  e4m3 rows come through registers, a tile ahead,
+//     sixteen reach 17 TB/s from L2 and 7 TB/s from memory in a kernel of
+//     such copies alone, eight 14.5 and 5.7, four 8.7 and 3.3.  e4m3 rows come through registers, a tile ahead,
 //     and are written as bf16 (exact);
 //   * the MMA warp issues S(t+1) before O(t), so that the tensor pipe has
 //     work while the softmax of a tile runs;
@@ -37,7 +39,8 @@
 // whether it holds is one vote a tile, taken behind the exponentials.  When
 // it fails (always in the first tile) the rows' true maxima become the new
 // reference, and O and the row sums are scaled once.  Weights lie in
-// [0, 2^16], where floating point is as exact as in [0, 1].
+// [0, 2^16], where floating point is as exact as in [0, 1]; sums of weights and
+// values stay finite for values below 2^112 over the number of tokens.
 //
 // The matrix unit takes weights in bf16.  One rounding (2^-8 of a weight at
 // most) would leave outputs 1.4 times as far off as their own rounding to bf16

@@ -1,6 +1,6 @@
 // dsa_paged.cuh — what the paged-cache kernels share: the argument block, the
-// request a query row belongs to, the slot of a position, and the merge of
-// partial softmax results.
+// request a query row belongs to, the slot of a position, and what a NaN or an
+// empty row does to a softmax.
 #pragma once
 
 #include "dsa_common.cuh"
